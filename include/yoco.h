@@ -289,6 +289,136 @@ yoco_status yoco_gret_prefill(const void *q, const void *k, const void *v, const
 yoco_status yoco_gret_decode(const void *q, const void *k, const void *v, const float *g, int32_t B,
                              float tau, float *state, void *o, const yoco_attn_cfg *cfg, cudaStream_t stream);
 
+/* Rotary positions of Q and K.  The attention calls take Q and K that carry
+ * their positions; this call puts them there (the pages give the rotary base
+ * only: "You Only Cache Once", paperlayer summary, Appendix C).
+ * The first rot_dim elements of every head are rot_dim / 2 pairs (a, b):
+ * elements i and i + rot_dim / 2 (YOCO_ROPE_HALF), or 2 i and 2 i + 1
+ * (YOCO_ROPE_INTERLEAVED).  Pair i of a token at position p turns by
+ * t = p inv_freq[i]:  a' = mscale (a cos t - b sin t),
+ * b' = mscale (b cos t + a sin t).  The other elements stay as they are.
+ * t is formed in 64 bits; the products are fp32, rounded once.
+ *
+ * yoco_rope_cfg is host memory, filled by yoco_rope_init or by the caller:
+ * rot_dim a multiple of 16 in [16, D], inv_freq in radians a position (the
+ * first rot_dim / 2 are read).
+ *
+ * yoco_rope_init: inv_freq[i] = w_i = theta^(-2 i / rot_dim), scaled by
+ *   YOCO_ROPE_NONE      as they are (factor is not read);
+ *   YOCO_ROPE_LINEAR    w_i / factor;
+ *   YOCO_ROPE_NTK       theta becomes theta factor^(rot_dim / (rot_dim - 2));
+ *   YOCO_ROPE_BY_PARTS  g w_i + (1 - g) w_i / factor, where
+ *                       r = orig_len w_i / 2 pi is the pair's turns over the
+ *                       original context and
+ *                       g = clamp((r - beta_slow) / (beta_fast - beta_slow), 0, 1).
+ * mscale 0 means 0.1 ln(factor) + 1 for YOCO_ROPE_BY_PARTS and 1 otherwise.
+ * Host only.  YOCO_ERR_INVALID: rot_dim not a multiple of 16 in [16, 128],
+ * theta <= 0 or not finite, factor < 1 or not finite (when read), for
+ * YOCO_ROPE_BY_PARTS orig_len <= 0 or not beta_slow < beta_fast, a negative
+ * or infinite mscale, an unknown layout or scaling.
+ *
+ * yoco_rope: q [B, T, Hq, D], k [B, T, Hkv, D] (either may be NULL, with its
+ * output; a decode step has T = 1); q_out, k_out like q, k: the same buffer (in
+ * place) or one that does not overlap it.  pos: device int64 [B, T], or NULL:
+ * token t of every sequence is at pos0 + t.  backward nonzero: q and k are the
+ * gradients of the rotated Q and K, and the outputs the gradients before the
+ * rotation (the turn by -t, with the same mscale).
+ * YOCO_ERR_UNSUPPORTED: rot_dim > D. */
+enum { YOCO_ROPE_HALF = 0, YOCO_ROPE_INTERLEAVED = 1 };
+enum { YOCO_ROPE_NONE = 0, YOCO_ROPE_LINEAR = 1, YOCO_ROPE_NTK = 2, YOCO_ROPE_BY_PARTS = 3 };
+typedef struct {
+    int32_t rot_dim;
+    int32_t layout;
+    double mscale;
+    double inv_freq[64];
+} yoco_rope_cfg;
+yoco_status yoco_rope_init(yoco_rope_cfg *rope, int32_t rot_dim, int32_t layout, double theta, int32_t scaling,
+                           double factor, double orig_len, double beta_fast, double beta_slow, double mscale);
+yoco_status yoco_rope(const void *q, const void *k, int32_t B, int64_t T, const int64_t *pos, int64_t pos0,
+                      int32_t backward, void *q_out, void *k_out, const yoco_rope_cfg *rope,
+                      const yoco_attn_cfg *cfg, cudaStream_t stream);
+
+/* Drafted tokens.  A decoder that drafts several tokens ahead (a chain, or a
+ * tree of alternatives) checks all of them in one pass: the nodes' Q, K, V are
+ * formed like any new tokens' (yoco_linear, yoco_kv_project_blend, yoco_rope
+ * at each node's position), every self-decoder layer runs
+ * yoco_swa_decode_tree and every cross-decoder layer yoco_cross_decode_tree,
+ * the caller accepts a path of nodes, and the commits below write its K / V
+ * where the next step's decodes read them.  Until then neither the shared
+ * cache nor a ring is written.  The pages do not draft; the context read is
+ * theirs (podcast cue 26, section 3).
+ *
+ * Shared by both trees
+ *  - q, o [B, N, Hq, D]; k_nodes, v_nodes [B, N, Hkv, D]; 1 <= N <= 64
+ *    (YOCO_ERR_UNSUPPORTED above).
+ *  - tree_mask: device uint64 [B, N]: bit j of tree_mask[b][i] set lets node i
+ *    see node j (its ancestors, and itself: nothing is implied).  NULL: a
+ *    chain, node i sees nodes 0..i.
+ *  - n_nodes: device int32 [B] or NULL (N each): nodes from n_nodes[b] on do
+ *    not exist; nothing sees them and their rows come out as below.
+ *  - A row that sees no key, or whose node does not exist: o = 0, lse = -inf.
+ *    What an unseen key's K and V hold (infinities, NaN) has no effect.
+ *  - lse [B, Hq, N] or NULL.
+ *  - workspace: device scratch of the size query's bytes; it needs no clearing
+ *    and keeps nothing between calls, but calls whose kernels may overlap need
+ *    one each.  Two launches, no host synchronisation.
+ *  - A sequence whose device-side arguments are out of range (n_nodes outside
+ *    [0, N], or as stated below) reads nothing; its o is 0 and its lse -inf,
+ *    the others are computed, and the next yoco_get_device_status returns
+ *    YOCO_ERR_INVALID.
+ *
+ * yoco_cross_decode_tree: node i sees rows [seq_start[b], seq_start[b] +
+ * seq_len[b]) of the packed cache [cache_rows, Hkv, D] (the committed tokens;
+ * unlike in yoco_cross_decode the new tokens are not among them) and its
+ * nodes.  In range: 0 <= seq_len <= max_len, rows inside the cache.
+ * max_len >= 0 (host) sizes the plan. */
+yoco_status yoco_cross_decode_tree(const void *q, const void *k_nodes, const void *v_nodes, const void *k_cache,
+                                   const void *v_cache, int64_t cache_rows, const int64_t *seq_start,
+                                   const int32_t *seq_len, const uint64_t *tree_mask, const int32_t *n_nodes,
+                                   int32_t B, int32_t N, int64_t max_len, void *o, float *lse, void *workspace,
+                                   size_t ws_bytes, const yoco_attn_cfg *cfg, cudaStream_t stream);
+size_t yoco_cross_decode_tree_workspace_size(int32_t B, int32_t N, int64_t max_len, const yoco_attn_cfg *cfg);
+
+/* yoco_swa_decode_tree: the self-decoder's counterpart over the ring
+ * (ring_k, ring_v [B, window, Hkv, D], slot_pos int32 [B, window], read only).
+ * node_pos: device int64 [B, N], the absolute positions.  Node i at position p
+ * sees the slots whose stored position s has s >= 0 and p - window < s < p, and
+ * of its nodes those at a position in (p - window, p]. */
+yoco_status yoco_swa_decode_tree(const void *q, const void *k_nodes, const void *v_nodes, const int64_t *node_pos,
+                                 const uint64_t *tree_mask, const int32_t *n_nodes, int32_t B, int32_t N,
+                                 int32_t window, const void *ring_k, const void *ring_v, const int32_t *slot_pos,
+                                 void *o, float *lse, void *workspace, size_t ws_bytes, const yoco_attn_cfg *cfg,
+                                 cudaStream_t stream);
+size_t yoco_swa_decode_tree_workspace_size(int32_t B, int32_t N, int32_t window, const yoco_attn_cfg *cfg);
+
+/* The accepted path of each sequence: path device int32 [B, N], n_path device
+ * int32 [B]; nodes path[b][0 .. n_path[b]) in order (later entries are not
+ * read).  A sequence out of range (n_path outside [0, N], an entry outside
+ * [0, N), or as stated below) is left as it is, and the next
+ * yoco_get_device_status returns YOCO_ERR_INVALID.  cfg->Hq and cfg->scale
+ * are not read beyond the usual checks.
+ *
+ * yoco_cross_tree_commit: node path[j]'s K / V become cache row seq_start +
+ * seq_len + j, and new_len[b] (device int32 [B], not seq_len itself) =
+ * seq_len + n_path.  seq_cap: device int32 [B], the most rows each sequence may
+ * have, or NULL: the caller has made sure that the rows behind a sequence are
+ * its own.  In range: seq_len >= 0, seq_len + n_path <= seq_cap, rows inside
+ * the cache; a sequence out of range keeps new_len = seq_len.  With N = 1 and
+ * path 0 this appends one new token to every sequence.
+ *
+ * yoco_swa_tree_commit: node path[j]'s K / V go to ring slot p mod window, p =
+ * node_pos[b][path[j]], and slot_pos there becomes p; of entries that share a
+ * slot the last one stays.  In range: 0 <= p <= 2^31 - 1. */
+yoco_status yoco_cross_tree_commit(const void *k_nodes, const void *v_nodes, const int32_t *path,
+                                   const int32_t *n_path, int32_t B, int32_t N, void *k_cache, void *v_cache,
+                                   int64_t cache_rows, const int64_t *seq_start, const int32_t *seq_len,
+                                   const int32_t *seq_cap, int32_t *new_len, const yoco_attn_cfg *cfg,
+                                   cudaStream_t stream);
+yoco_status yoco_swa_tree_commit(const void *k_nodes, const void *v_nodes, const int64_t *node_pos,
+                                 const int32_t *path, const int32_t *n_path, int32_t B, int32_t N, int32_t window,
+                                 void *ring_k, void *ring_v, int32_t *slot_pos, const yoco_attn_cfg *cfg,
+                                 cudaStream_t stream);
+
 /* Test-only, with no counterpart on the pages: the work plan the kernels
  * follow, computed on the host by the kernels' own schedule functions, so
  * that tests can check it against the visibility rule pair by pair.  Reads
@@ -327,8 +457,8 @@ double yoco_cache_bytes(int32_t L_self, int32_t window, int64_t N, const yoco_at
 
 /* Synchronises the stream, then returns and clears the device status word:
  * YOCO_ERR_TIMEOUT if a kernel's bounded wait gave up since the last call,
- * else YOCO_ERR_INVALID if a decode call met a sequence out of range (see
- * yoco_cross_decode), else YOCO_ERR_CUDA if the stream reports an error,
+ * else YOCO_ERR_INVALID if a decode or commit call met a sequence out of range
+ * (see yoco_cross_decode), else YOCO_ERR_CUDA if the stream reports an error,
  * else YOCO_OK. */
 yoco_status yoco_get_device_status(cudaStream_t stream);
 

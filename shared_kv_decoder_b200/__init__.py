@@ -11,10 +11,13 @@ Entry points (same names as the C ABI, without the ``yoco_`` prefix):
 kv_project_blend, swa_prefill, swa_decode, cross_prefill, cross_decode,
 attention_prefill,
 gret_prefill, gret_decode, kv_quantize_i8, cross_decode_i8,
+rope (with rope_config), cross_decode_tree, swa_decode_tree, cross_tree_commit,
+swa_tree_commit,
 plus linear, workspace sizes, cache_bytes, device_status and the test-only
 debug_tile_schedule.
 """
 import ctypes
+import functools
 import os
 
 import torch
@@ -25,7 +28,9 @@ __all__ = ["YocoError", "load", "lib_path", "kv_project_blend", "linear", "swa_p
            "swa_decode_workspace_size", "cache_bytes", "device_status", "launch_count", "AttnCfg",
            "debug_tile_schedule", "SCHEDULE_PREFILL", "SCHEDULE_DECODE", "gret_prefill", "gret_decode",
            "kv_i8_row_bytes", "kv_quantize_i8", "cross_decode_i8",
-           "attention_prefill", "debug_exp2_poly", "gret_prefill_workspace_size"]
+           "attention_prefill", "debug_exp2_poly", "gret_prefill_workspace_size",
+           "RopeCfg", "rope_config", "rope", "cross_decode_tree", "cross_decode_tree_workspace_size",
+           "swa_decode_tree", "swa_decode_tree_workspace_size", "cross_tree_commit", "swa_tree_commit"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB = None
@@ -48,6 +53,16 @@ class AttnCfg(ctypes.Structure):
                 ("scale", ctypes.c_float), ("dtype", ctypes.c_int32)]
 
 
+class RopeCfg(ctypes.Structure):
+    """yoco_rope_cfg: what yoco_rope turns by (rope_config fills one)."""
+    _fields_ = [("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("mscale", ctypes.c_double),
+                ("inv_freq", ctypes.c_double * 64)]
+
+
+_ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+_ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
+
+
 def lib_path():
     return os.path.join(_HERE, "libyoco.so")
 
@@ -64,6 +79,7 @@ def load():
     L = ctypes.CDLL(path)
     vp, i32, i64, f32, sz = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float,
                              ctypes.c_size_t)
+    f64 = ctypes.c_double
     cfgp = ctypes.POINTER(AttnCfg)
     st = ctypes.c_int
     sigs = {
@@ -88,6 +104,15 @@ def load():
         "yoco_kv_quantize_i8": (st, [vp, vp, i64, vp, vp, vp, cfgp, vp]),
         "yoco_cross_decode_i8": (st, [vp, vp, vp, i64, vp, vp, i32, i64, vp, vp, vp, sz, cfgp, vp]),
         "yoco_gret_decode": (st, [vp, vp, vp, vp, i32, f32, vp, vp, cfgp, vp]),
+        "yoco_rope_init": (st, [ctypes.POINTER(RopeCfg), i32, i32, f64, i32, f64, f64, f64, f64, f64]),
+        "yoco_rope": (st, [vp, vp, i32, i64, vp, i64, i32, vp, vp, ctypes.POINTER(RopeCfg), cfgp, vp]),
+        "yoco_cross_decode_tree": (st, [vp, vp, vp, vp, vp, i64, vp, vp, vp, vp, i32, i32, i64, vp, vp, vp, sz, cfgp,
+                                        vp]),
+        "yoco_cross_decode_tree_workspace_size": (sz, [i32, i32, i64, cfgp]),
+        "yoco_swa_decode_tree": (st, [vp, vp, vp, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp, vp, vp, sz, cfgp, vp]),
+        "yoco_swa_decode_tree_workspace_size": (sz, [i32, i32, i32, cfgp]),
+        "yoco_cross_tree_commit": (st, [vp, vp, vp, vp, i32, i32, vp, vp, i64, vp, vp, vp, vp, cfgp, vp]),
+        "yoco_swa_tree_commit": (st, [vp, vp, vp, vp, vp, i32, i32, i32, vp, vp, vp, cfgp, vp]),
         "yoco_debug_tile_schedule": (st, [i32, cfgp, i32, i64, i64, i64, i32, vp, vp, i64, i32, vp,
                                           i64, ctypes.POINTER(ctypes.c_int64)]),
         "yoco_get_device_status": (st, [vp]),
@@ -437,3 +462,227 @@ def debug_exp2_poly(x, y=None):
         raise ValueError("debug_exp2_poly takes fp32 tensors of one size")
     _check(L.yoco_debug_exp2_poly(_ptr(x), _ptr(y), x.numel(), _stream()), "yoco_debug_exp2_poly")
     return y
+
+
+# ---------------------------------------------- rotary positions, drafted tokens
+def _want(t, name, dtypes, shape, device):
+    """One tensor argument: its type, shape, device and layout."""
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError("libyoco takes contiguous tensors only")
+
+
+def _cuda_float(t, name):
+    if not t.is_cuda:
+        raise ValueError("libyoco takes CUDA tensors only")
+    if t.dtype not in _DT:
+        raise ValueError(f"{name}: {t.dtype}, expected {' or '.join(str(d) for d in _DT)}")
+    return t.device
+
+
+_I32, _I64, _MASK = (torch.int32,), (torch.int64,), (torch.int64, torch.uint64)
+
+
+@functools.lru_cache(maxsize=256)
+def _cfg_ref(Hq, Hkv, D, dtype, scale=0.0):
+    return ctypes.byref(_cfg(Hq, Hkv, D, dtype, scale))
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _call(device, name, *args):
+    """A library call on `device` and its current stream."""
+    fn = getattr(load(), name)
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if status != OK:
+        raise YocoError(status, name)
+
+
+def rope_config(rot_dim, theta=10000.0, layout="half", scaling="none", factor=1.0, orig_len=0, beta_fast=32.0,
+                beta_slow=1.0, mscale=0.0):
+    """The pairs, frequencies and magnitude that rope() turns by.  layout
+    "half" (elements i, i + rot_dim / 2) or "interleaved" (2i, 2i + 1); scaling
+    "none", "linear", "ntk" or "by_parts" (its mscale 0: 0.1 ln(factor) + 1).
+    The returned RopeCfg's inv_freq (radians a position) may be set freely."""
+    if layout not in _ROPE_LAYOUTS or scaling not in _ROPE_SCALINGS:
+        raise ValueError(f"layout is one of {list(_ROPE_LAYOUTS)}, scaling one of {list(_ROPE_SCALINGS)}")
+    cfg = RopeCfg()
+    _check(load().yoco_rope_init(ctypes.byref(cfg), int(rot_dim), _ROPE_LAYOUTS[layout], float(theta),
+                                 _ROPE_SCALINGS[scaling], float(factor), float(orig_len), float(beta_fast),
+                                 float(beta_slow), float(mscale)), "yoco_rope_init")
+    return cfg
+
+
+def rope(q, k, rope_cfg, pos=None, pos0=0, q_out=None, k_out=None, backward=False):
+    """Rotary positions.  q [B, T, Hq, D] and k [B, T, Hkv, D], or one token a
+    sequence as [B, Hq, D] and [B, Hkv, D]; either may be None.  pos int64
+    [B, T] ([B]); None: token t of every sequence is at pos0 + t.  backward: q
+    and k are gradients of the rotated Q and K, the result those before it.
+    Returns (q_out, k_out), new tensors unless given (q_out = q: in place)."""
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("rope needs q or k")
+    device = _cuda_float(x, "q" if q is not None else "k")
+    lead = x.shape[:-2]
+    if len(lead) not in (1, 2):
+        raise ValueError("rope takes [B, T, heads, D] or [B, heads, D]")
+    B, T = lead if len(lead) == 2 else (lead[0], 1)
+    D = x.shape[-1]
+    Hq = Hkv = x.shape[-2]
+    if q is not None:
+        _want(q, "q", (x.dtype,), (*lead, Hq, D), device)
+        q_out = torch.empty_like(q) if q_out is None else q_out
+        _want(q_out, "q_out", (x.dtype,), q.shape, device)
+    if k is not None:
+        Hkv = k.shape[-2]
+        _want(k, "k", (x.dtype,), (*lead, Hkv, D), device)
+        k_out = torch.empty_like(k) if k_out is None else k_out
+        _want(k_out, "k_out", (x.dtype,), k.shape, device)
+    if (q is None) != (q_out is None) or (k is None) != (k_out is None):
+        raise ValueError("an output without its input")
+    if pos is not None:
+        _want(pos, "pos", _I64, lead, device)
+    _call(device, "yoco_rope", _addr(q), _addr(k), B, T, _addr(pos), int(pos0), int(bool(backward)), _addr(q_out),
+          _addr(k_out), ctypes.byref(rope_cfg), _cfg_ref(Hq, Hkv, D, x.dtype))
+    return q_out, k_out
+
+
+@functools.lru_cache(maxsize=1024)
+def _tree_ws(device_index, B, N, max_len, Hq, Hkv, D, dtype):
+    with torch.cuda.device(device_index):
+        return int(load().yoco_cross_decode_tree_workspace_size(B, N, max_len, _cfg_ref(Hq, Hkv, D, dtype)))
+
+
+def cross_decode_tree_workspace_size(B, N, max_len, Hq, Hkv, D, dtype):
+    return int(load().yoco_cross_decode_tree_workspace_size(B, N, int(max_len), _cfg_ref(Hq, Hkv, D, dtype)))
+
+
+def swa_decode_tree_workspace_size(B, N, window, Hq, Hkv, D, dtype):
+    return int(load().yoco_swa_decode_tree_workspace_size(B, N, int(window), _cfg_ref(Hq, Hkv, D, dtype)))
+
+
+def _tree_args(q, k_nodes, v_nodes, tree_mask, n_nodes, context, workspace, o, want_lse):
+    """What both trees check and allocate: (B, N, Hkv, device, workspace, o, lse)."""
+    device = _cuda_float(q, "q")
+    if q.dim() != 4 or k_nodes.dim() != 4:
+        raise ValueError("q is [B, N, Hq, D], k_nodes and v_nodes [B, N, Hkv, D]")
+    B, N, Hq, D = q.shape
+    Hkv = k_nodes.shape[2]
+    own = (q.dtype,)
+    _want(q, "q", own, q.shape, device)
+    _want(k_nodes, "k_nodes", own, (B, N, Hkv, D), device)
+    _want(v_nodes, "v_nodes", own, (B, N, Hkv, D), device)
+    if tree_mask is not None:
+        _want(tree_mask, "tree_mask", _MASK, (B, N), device)
+    if n_nodes is not None:
+        _want(n_nodes, "n_nodes", _I32, (B,), device)
+    if workspace is None:
+        workspace = torch.empty(_tree_ws(device.index, B, N, context, Hq, Hkv, D, q.dtype), dtype=torch.uint8,
+                                device=device)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace: a contiguous tensor on {device}")
+    if o is None:
+        o = torch.empty_like(q)
+    else:
+        _want(o, "o", own, q.shape, device)
+    lse = torch.empty((B, Hq, N), dtype=torch.float32, device=device) if want_lse else None
+    return B, N, Hq, Hkv, D, device, workspace, o, lse
+
+
+def cross_decode_tree(q, k_nodes, v_nodes, k_cache, v_cache, seq_start, seq_len, max_len, tree_mask=None,
+                      n_nodes=None, workspace=None, want_lse=False, scale=0.0, o=None):
+    """Attention of drafted tokens over the packed shared cache.  q [B, N, Hq, D];
+    k_nodes, v_nodes [B, N, Hkv, D]; caches [rows, Hkv, D]; seq_start int64 [B];
+    seq_len int32 [B] (committed tokens); tree_mask int64 / uint64 [B, N]: bit j
+    lets node i see node j (None: a chain); n_nodes int32 [B] or None (N).
+    Returns o (and lse [B, Hq, N] when want_lse)."""
+    B, N, Hq, Hkv, D, device, workspace, o, lse = _tree_args(q, k_nodes, v_nodes, tree_mask, n_nodes, int(max_len),
+                                                             workspace, o, want_lse)
+    rows = (k_cache.shape[0], Hkv, D)
+    _want(k_cache, "k_cache", (q.dtype,), rows, device)
+    _want(v_cache, "v_cache", (q.dtype,), rows, device)
+    _want(seq_start, "seq_start", _I64, (B,), device)
+    _want(seq_len, "seq_len", _I32, (B,), device)
+    _call(device, "yoco_cross_decode_tree", q.data_ptr(), k_nodes.data_ptr(), v_nodes.data_ptr(), k_cache.data_ptr(),
+          v_cache.data_ptr(), rows[0], seq_start.data_ptr(), seq_len.data_ptr(), _addr(tree_mask), _addr(n_nodes), B, N,
+          int(max_len), o.data_ptr(), _addr(lse), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+          _cfg_ref(Hq, Hkv, D, q.dtype, float(scale)))
+    return (o, lse) if want_lse else o
+
+
+def swa_decode_tree(q, k_nodes, v_nodes, node_pos, ring_k, ring_v, slot_pos, window, tree_mask=None, n_nodes=None,
+                    workspace=None, want_lse=False, scale=0.0, o=None):
+    """Attention of drafted tokens over the sliding-window ring, which is only
+    read.  node_pos int64 [B, N]; ring_k, ring_v [B, window, Hkv, D]; slot_pos
+    int32 [B, window]; the rest as in cross_decode_tree."""
+    W = int(window)
+    B, N, Hq, Hkv, D, device, workspace, o, lse = _tree_args(q, k_nodes, v_nodes, tree_mask, n_nodes, W, workspace, o,
+                                                             want_lse)
+    _want(node_pos, "node_pos", _I64, (B, N), device)
+    _want(ring_k, "ring_k", (q.dtype,), (B, W, Hkv, D), device)
+    _want(ring_v, "ring_v", (q.dtype,), (B, W, Hkv, D), device)
+    _want(slot_pos, "slot_pos", _I32, (B, W), device)
+    _call(device, "yoco_swa_decode_tree", q.data_ptr(), k_nodes.data_ptr(), v_nodes.data_ptr(), node_pos.data_ptr(),
+          _addr(tree_mask), _addr(n_nodes), B, N, W, ring_k.data_ptr(), ring_v.data_ptr(), slot_pos.data_ptr(),
+          o.data_ptr(), _addr(lse), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+          _cfg_ref(Hq, Hkv, D, q.dtype, float(scale)))
+    return (o, lse) if want_lse else o
+
+
+def _commit_args(k_nodes, v_nodes, path, n_path):
+    device = _cuda_float(k_nodes, "k_nodes")
+    if k_nodes.dim() != 4:
+        raise ValueError("k_nodes and v_nodes are [B, N, Hkv, D]")
+    B, N = k_nodes.shape[:2]
+    _want(k_nodes, "k_nodes", (k_nodes.dtype,), k_nodes.shape, device)
+    _want(v_nodes, "v_nodes", (k_nodes.dtype,), k_nodes.shape, device)
+    _want(path, "path", _I32, (B, N), device)
+    _want(n_path, "n_path", _I32, (B,), device)
+    return (*k_nodes.shape, device)
+
+
+def cross_tree_commit(k_nodes, v_nodes, path, n_path, k_cache, v_cache, seq_start, seq_len, seq_cap=None, new_len=None):
+    """Appends the accepted nodes path[b][:n_path[b]] (int32 [B, N], [B]) to each
+    sequence of the packed cache; seq_cap int32 [B] bounds a sequence's rows.
+    Returns new_len int32 [B]; seq_len stays as it is."""
+    B, N, Hkv, D, device = _commit_args(k_nodes, v_nodes, path, n_path)
+    rows = (k_cache.shape[0], Hkv, D)
+    _want(k_cache, "k_cache", (k_nodes.dtype,), rows, device)
+    _want(v_cache, "v_cache", (k_nodes.dtype,), rows, device)
+    _want(seq_start, "seq_start", _I64, (B,), device)
+    _want(seq_len, "seq_len", _I32, (B,), device)
+    if seq_cap is not None:
+        _want(seq_cap, "seq_cap", _I32, (B,), device)
+    if new_len is None:
+        new_len = torch.empty_like(seq_len)
+    else:
+        _want(new_len, "new_len", _I32, (B,), device)
+    _call(device, "yoco_cross_tree_commit", k_nodes.data_ptr(), v_nodes.data_ptr(), path.data_ptr(), n_path.data_ptr(),
+          B, N, k_cache.data_ptr(), v_cache.data_ptr(), rows[0], seq_start.data_ptr(), seq_len.data_ptr(),
+          _addr(seq_cap), new_len.data_ptr(), _cfg_ref(Hkv, Hkv, D, k_nodes.dtype))
+    return new_len
+
+
+def swa_tree_commit(k_nodes, v_nodes, node_pos, path, n_path, ring_k, ring_v, slot_pos, window):
+    """Pushes the accepted nodes path[b][:n_path[b]] into the ring, in order:
+    slot node_pos mod window, slot_pos updated."""
+    B, N, Hkv, D, device = _commit_args(k_nodes, v_nodes, path, n_path)
+    W = int(window)
+    _want(node_pos, "node_pos", _I64, (B, N), device)
+    _want(ring_k, "ring_k", (k_nodes.dtype,), (B, W, Hkv, D), device)
+    _want(ring_v, "ring_v", (k_nodes.dtype,), (B, W, Hkv, D), device)
+    _want(slot_pos, "slot_pos", _I32, (B, W), device)
+    _call(device, "yoco_swa_tree_commit", k_nodes.data_ptr(), v_nodes.data_ptr(), node_pos.data_ptr(), path.data_ptr(),
+          n_path.data_ptr(), B, N, W, ring_k.data_ptr(), ring_v.data_ptr(), slot_pos.data_ptr(),
+          _cfg_ref(Hkv, Hkv, D, k_nodes.dtype))

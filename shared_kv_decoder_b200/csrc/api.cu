@@ -401,6 +401,166 @@ yoco_status yoco_gret_decode(const void *q, const void *k, const void *v, const 
     return from_cuda(launch_gret_decode(a, stream));
 }
 
+yoco_status yoco_rope_init(yoco_rope_cfg *rope, int32_t rot_dim, int32_t layout, double theta, int32_t scaling,
+                           double factor, double orig_len, double beta_fast, double beta_slow, double mscale) {
+    if (!rope || rot_dim < 16 || rot_dim > 128 || rot_dim % 16 != 0) return YOCO_ERR_INVALID;
+    if (layout != YOCO_ROPE_HALF && layout != YOCO_ROPE_INTERLEAVED) return YOCO_ERR_INVALID;
+    if (scaling < YOCO_ROPE_NONE || scaling > YOCO_ROPE_BY_PARTS) return YOCO_ERR_INVALID;
+    if (!(theta > 0.0) || isinf(theta) || !(mscale >= 0.0) || isinf(mscale)) return YOCO_ERR_INVALID;
+    if (scaling != YOCO_ROPE_NONE && (!(factor >= 1.0) || isinf(factor))) return YOCO_ERR_INVALID;
+    if (scaling == YOCO_ROPE_BY_PARTS &&
+        (!(orig_len > 0.0) || isinf(orig_len) || !(beta_slow < beta_fast) || isinf(beta_slow) || isinf(beta_fast)))
+        return YOCO_ERR_INVALID;
+    constexpr double kTwoPi = 6.283185307179586476925;
+    const double base = scaling == YOCO_ROPE_NTK ? theta * pow(factor, rot_dim / (rot_dim - 2.0)) : theta;
+    rope->rot_dim = rot_dim;
+    rope->layout = layout;
+    rope->mscale = mscale > 0.0 ? mscale : scaling == YOCO_ROPE_BY_PARTS ? 0.1 * log(factor) + 1.0 : 1.0;
+    for (int i = 0; i < 64; ++i) {
+        double w = i < rot_dim / 2 ? pow(base, -2.0 * i / rot_dim) : 0.0;
+        if (scaling == YOCO_ROPE_LINEAR) w /= factor;
+        if (scaling == YOCO_ROPE_BY_PARTS) {
+            const double r = orig_len * w / kTwoPi;
+            const double g = std::min(1.0, std::max(0.0, (r - beta_slow) / (beta_fast - beta_slow)));
+            w = g * w + (1.0 - g) * w / factor;
+        }
+        rope->inv_freq[i] = w;
+    }
+    return YOCO_OK;
+}
+
+yoco_status yoco_rope(const void *q, const void *k, int32_t B, int64_t T, const int64_t *pos, int64_t pos0,
+                      int32_t backward, void *q_out, void *k_out, const yoco_rope_cfg *rope,
+                      const yoco_attn_cfg *cfg, cudaStream_t stream) {
+    yoco_status st = check_cfg(cfg);
+    if (st != YOCO_OK) return st;
+    if (!rope || rope->rot_dim < 16 || rope->rot_dim > 128 || rope->rot_dim % 16 != 0 ||
+        (rope->layout != YOCO_ROPE_HALF && rope->layout != YOCO_ROPE_INTERLEAVED) || !isfinite(rope->mscale))
+        return YOCO_ERR_INVALID;
+    for (int i = 0; i < rope->rot_dim / 2; ++i)
+        if (!isfinite(rope->inv_freq[i])) return YOCO_ERR_INVALID;
+    if (rope->rot_dim > cfg->D) return YOCO_ERR_UNSUPPORTED;
+    if (B < 0 || T < 0 || (T > 0 && B > INT64_MAX / T)) return YOCO_ERR_INVALID;
+    if ((q != nullptr) != (q_out != nullptr) || (k != nullptr) != (k_out != nullptr)) return YOCO_ERR_INVALID;
+    if (B == 0 || T == 0) return YOCO_OK;
+    if ((!q && !k) || !ok_opt(q) || !ok_opt(k) || !ok_opt(q_out) || !ok_opt(k_out) || !ok_opt(pos))
+        return YOCO_ERR_INVALID;
+    RopeArgs a;
+    a.q = q; a.k = k; a.q_out = q_out; a.k_out = k_out; a.pos = pos;
+    a.n = B * T; a.T = T; a.pos0 = pos0;
+    a.Hq = cfg->Hq; a.Hkv = cfg->Hkv; a.D = cfg->D; a.dtype = cfg->dtype;
+    a.rot_dim = rope->rot_dim; a.interleaved = rope->layout == YOCO_ROPE_INTERLEAVED; a.backward = backward != 0;
+    a.mscale = (float)rope->mscale; a.inv_freq = rope->inv_freq;
+    return from_cuda(launch_rope(a, stream));
+}
+
+size_t yoco_cross_decode_tree_workspace_size(int32_t B, int32_t N, int64_t max_len, const yoco_attn_cfg *cfg) {
+    if (check_cfg(cfg) != YOCO_OK || B < 1 || N < 1 || N > kTreeMaxNodes || max_len < 0 || max_len > INT32_MAX) return 0;
+    TreePlan pl;
+    if (!make_tree_plan(B, N, max_len, cfg->Hq, cfg->Hkv, cfg->D, cfg->dtype, &pl)) return 0;
+    return pl.ws_bytes;
+}
+
+size_t yoco_swa_decode_tree_workspace_size(int32_t B, int32_t N, int32_t window, const yoco_attn_cfg *cfg) {
+    if (window < 1) return 0;
+    return yoco_cross_decode_tree_workspace_size(B, N, window, cfg);
+}
+
+yoco_status yoco_cross_decode_tree(const void *q, const void *k_nodes, const void *v_nodes, const void *k_cache,
+                                   const void *v_cache, int64_t cache_rows, const int64_t *seq_start,
+                                   const int32_t *seq_len, const uint64_t *tree_mask, const int32_t *n_nodes,
+                                   int32_t B, int32_t N, int64_t max_len, void *o, float *lse, void *workspace,
+                                   size_t ws_bytes, const yoco_attn_cfg *cfg, cudaStream_t stream) {
+    yoco_status st = check_cfg(cfg);
+    if (st != YOCO_OK) return st;
+    if (B < 0 || N < 1 || max_len < 0 || max_len > INT32_MAX || !ok_cache_rows(cache_rows)) return YOCO_ERR_INVALID;
+    if (N > kTreeMaxNodes) return YOCO_ERR_UNSUPPORTED;
+    if (B == 0) return YOCO_OK;
+    if (!ok_ptr(q) || !ok_ptr(k_nodes) || !ok_ptr(v_nodes) || !ok_ptr(k_cache) || !ok_ptr(v_cache) ||
+        !ok_ptr(seq_start) || !ok_ptr(seq_len) || !ok_opt(tree_mask) || !ok_opt(n_nodes) || !ok_ptr(o) || !ok_opt(lse))
+        return YOCO_ERR_INVALID;
+    TreePlan pl;
+    if (!make_tree_plan(B, N, max_len, cfg->Hq, cfg->Hkv, cfg->D, cfg->dtype, &pl)) return YOCO_ERR_UNSUPPORTED;
+    if (!ok_ptr(workspace) || ws_bytes < pl.ws_bytes) return YOCO_ERR_WORKSPACE;
+    TreeArgs a;
+    a.q = q; a.k_nodes = k_nodes; a.v_nodes = v_nodes; a.k = k_cache; a.v = v_cache;
+    a.seq_start = seq_start; a.seq_len = seq_len; a.slot_pos = nullptr; a.node_pos = nullptr;
+    a.mask = tree_mask; a.n_nodes = n_nodes; a.B = B; a.N = N;
+    a.Hq = cfg->Hq; a.Hkv = cfg->Hkv; a.D = cfg->D; a.dtype = cfg->dtype;
+    a.window = 0; a.cache_rows = cache_rows; a.max_len = max_len;
+    a.scale = eff_scale(cfg); a.o = o; a.lse = lse; a.ws = workspace;
+    return from_cuda(launch_tree(a, pl, stream));
+}
+
+yoco_status yoco_swa_decode_tree(const void *q, const void *k_nodes, const void *v_nodes, const int64_t *node_pos,
+                                 const uint64_t *tree_mask, const int32_t *n_nodes, int32_t B, int32_t N,
+                                 int32_t window, const void *ring_k, const void *ring_v, const int32_t *slot_pos,
+                                 void *o, float *lse, void *workspace, size_t ws_bytes, const yoco_attn_cfg *cfg,
+                                 cudaStream_t stream) {
+    yoco_status st = check_cfg(cfg);
+    if (st != YOCO_OK) return st;
+    if (B < 0 || N < 1 || window < 1) return YOCO_ERR_INVALID;
+    if (N > kTreeMaxNodes) return YOCO_ERR_UNSUPPORTED;
+    if (B == 0) return YOCO_OK;
+    if (!ok_ptr(q) || !ok_ptr(k_nodes) || !ok_ptr(v_nodes) || !ok_ptr(node_pos) || !ok_opt(tree_mask) ||
+        !ok_opt(n_nodes) || !ok_ptr(ring_k) || !ok_ptr(ring_v) || !ok_ptr(slot_pos) || !ok_ptr(o) || !ok_opt(lse))
+        return YOCO_ERR_INVALID;
+    TreePlan pl;
+    if (!make_tree_plan(B, N, window, cfg->Hq, cfg->Hkv, cfg->D, cfg->dtype, &pl)) return YOCO_ERR_UNSUPPORTED;
+    if (!ok_ptr(workspace) || ws_bytes < pl.ws_bytes) return YOCO_ERR_WORKSPACE;
+    TreeArgs a;
+    a.q = q; a.k_nodes = k_nodes; a.v_nodes = v_nodes; a.k = ring_k; a.v = ring_v;
+    a.seq_start = nullptr; a.seq_len = nullptr; a.slot_pos = slot_pos; a.node_pos = node_pos;
+    a.mask = tree_mask; a.n_nodes = n_nodes; a.B = B; a.N = N;
+    a.Hq = cfg->Hq; a.Hkv = cfg->Hkv; a.D = cfg->D; a.dtype = cfg->dtype;
+    a.window = window; a.cache_rows = (int64_t)B * window; a.max_len = window;
+    a.scale = eff_scale(cfg); a.o = o; a.lse = lse; a.ws = workspace;
+    return from_cuda(launch_tree(a, pl, stream));
+}
+
+yoco_status yoco_cross_tree_commit(const void *k_nodes, const void *v_nodes, const int32_t *path,
+                                   const int32_t *n_path, int32_t B, int32_t N, void *k_cache, void *v_cache,
+                                   int64_t cache_rows, const int64_t *seq_start, const int32_t *seq_len,
+                                   const int32_t *seq_cap, int32_t *new_len, const yoco_attn_cfg *cfg,
+                                   cudaStream_t stream) {
+    yoco_status st = check_cfg(cfg);
+    if (st != YOCO_OK) return st;
+    if (B < 0 || N < 1 || !ok_cache_rows(cache_rows) || (new_len && new_len == seq_len)) return YOCO_ERR_INVALID;
+    if (N > kTreeMaxNodes) return YOCO_ERR_UNSUPPORTED;
+    if (B == 0) return YOCO_OK;
+    if (!ok_ptr(k_nodes) || !ok_ptr(v_nodes) || !ok_ptr(path) || !ok_ptr(n_path) || !ok_ptr(k_cache) ||
+        !ok_ptr(v_cache) || !ok_ptr(seq_start) || !ok_ptr(seq_len) || !ok_opt(seq_cap) || !ok_ptr(new_len))
+        return YOCO_ERR_INVALID;
+    CommitArgs a;
+    a.k_nodes = k_nodes; a.v_nodes = v_nodes; a.path = path; a.n_path = n_path; a.B = B; a.N = N;
+    a.row_bytes = (int64_t)cfg->Hkv * cfg->D * dtype_bytes(cfg->dtype);
+    a.k = k_cache; a.v = v_cache; a.seq_start = seq_start; a.seq_len = seq_len; a.seq_cap = seq_cap;
+    a.new_len = new_len; a.cache_rows = cache_rows;
+    a.node_pos = nullptr; a.slot_pos = nullptr; a.window = 0;
+    return from_cuda(launch_commit(a, stream));
+}
+
+yoco_status yoco_swa_tree_commit(const void *k_nodes, const void *v_nodes, const int64_t *node_pos,
+                                 const int32_t *path, const int32_t *n_path, int32_t B, int32_t N, int32_t window,
+                                 void *ring_k, void *ring_v, int32_t *slot_pos, const yoco_attn_cfg *cfg,
+                                 cudaStream_t stream) {
+    yoco_status st = check_cfg(cfg);
+    if (st != YOCO_OK) return st;
+    if (B < 0 || N < 1 || window < 1) return YOCO_ERR_INVALID;
+    if (N > kTreeMaxNodes) return YOCO_ERR_UNSUPPORTED;
+    if (B == 0) return YOCO_OK;
+    if (!ok_ptr(k_nodes) || !ok_ptr(v_nodes) || !ok_ptr(node_pos) || !ok_ptr(path) || !ok_ptr(n_path) ||
+        !ok_ptr(ring_k) || !ok_ptr(ring_v) || !ok_ptr(slot_pos))
+        return YOCO_ERR_INVALID;
+    CommitArgs a;
+    a.k_nodes = k_nodes; a.v_nodes = v_nodes; a.path = path; a.n_path = n_path; a.B = B; a.N = N;
+    a.row_bytes = (int64_t)cfg->Hkv * cfg->D * dtype_bytes(cfg->dtype);
+    a.k = ring_k; a.v = ring_v; a.seq_start = nullptr; a.seq_len = nullptr; a.seq_cap = nullptr;
+    a.new_len = nullptr; a.cache_rows = (int64_t)B * window;
+    a.node_pos = node_pos; a.slot_pos = slot_pos; a.window = window;
+    return from_cuda(launch_commit(a, stream));
+}
+
 yoco_status yoco_debug_tile_schedule(int32_t kind, const yoco_attn_cfg *cfg, int32_t B, int64_t Tq,
                                      int64_t Tkv, int64_t q_pos0, int32_t window,
                                      const int64_t *seq_start, const int32_t *seq_len, int64_t max_len,
@@ -494,7 +654,8 @@ yoco_status yoco_get_device_status(cudaStream_t stream) {
     const unsigned int s = read_and_clear_status_decode() | read_and_clear_status_prefill_tc() |
                            read_and_clear_status_prefill_pair() | read_and_clear_status_project_tc() |
                            read_and_clear_status_gret_tc() | read_and_clear_status_linear() |
-                           read_and_clear_status_ring() | read_and_clear_status_step_proj();
+                           read_and_clear_status_ring() | read_and_clear_status_step_proj() |
+                           read_and_clear_status_tree() | read_and_clear_status_commit();
     if (s & 1u) return YOCO_ERR_TIMEOUT;
     if (s & 2u) return YOCO_ERR_INVALID;
     return e == cudaSuccess ? YOCO_OK : YOCO_ERR_CUDA;

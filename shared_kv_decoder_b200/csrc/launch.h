@@ -130,12 +130,72 @@ cudaError_t launch_gret_prefill_tc(const GretArgs &a, cudaStream_t s);
 int gret_superchunks(int32_t B, int32_t H, int64_t T, int sms);
 size_t gret_workspace_bytes(int32_t B, int32_t H, int64_t T, int D);
 
+// ------------------------------------------------------- rotary positions
+struct RopeArgs {
+    const void *q, *k;        // [n, Hq, D], [n, Hkv, D]; k may be null
+    void *q_out, *k_out;
+    const int64_t *pos;       // [n] or null: token i at pos0 + i mod T
+    int64_t n, T, pos0;
+    int32_t Hq, Hkv, D, dtype;
+    int32_t rot_dim;
+    bool interleaved, backward;
+    float mscale;
+    const double *inv_freq;   // host, [rot_dim / 2], radians a position
+};
+cudaError_t launch_rope(const RopeArgs &a, cudaStream_t s);
+
+// -------------------------------------------------- drafted tokens (trees)
+constexpr int kTreeMaxNodes = 64;
+
+struct TreePlan {
+    int rows, keys;           // rows of a stream, keys of a tile (tree.cuh)
+    int grid;
+    size_t ml_off, o_off, ws_bytes;
+};
+// max_len: the longest context (a ring: its window).
+bool make_tree_plan(int32_t B, int32_t N, int64_t max_len, int Hq, int Hkv, int D, int dtype, TreePlan *plan);
+
+struct TreeArgs {
+    const void *q, *k_nodes, *v_nodes;
+    const void *k, *v;              // cache or ring
+    const int64_t *seq_start;       // cache only
+    const int32_t *seq_len;
+    const int32_t *slot_pos;        // ring only
+    const int64_t *node_pos;
+    const uint64_t *mask;           // or null
+    const int32_t *n_nodes;         // or null
+    int32_t B, N, Hq, Hkv, D, dtype;
+    int32_t window;                 // 0: cache
+    int64_t cache_rows, max_len;
+    float scale;
+    void *o;
+    float *lse;                     // or null
+    void *ws;
+};
+cudaError_t launch_tree(const TreeArgs &a, const TreePlan &plan, cudaStream_t s);
+
+struct CommitArgs {
+    const void *k_nodes, *v_nodes;  // [B, N, row]
+    const int32_t *path, *n_path;   // [B, N], [B]
+    int32_t B, N;
+    int64_t row_bytes;              // of one token's K (or V)
+    void *k, *v;                    // cache or ring
+    const int64_t *seq_start;       // cache only
+    const int32_t *seq_len, *seq_cap;
+    int32_t *new_len;
+    int64_t cache_rows;
+    const int64_t *node_pos;        // ring only
+    int32_t *slot_pos;
+    int32_t window;                 // 0: cache
+};
+cudaError_t launch_commit(const CommitArgs &a, cudaStream_t s);
+
 // Test-only: a kernel whose bounded wait is never satisfied (see decode.cu).
 cudaError_t launch_wait_timeout_probe(cudaStream_t s);
 
 // Device status words of the translation units that hold bounded waits:
-// bit 0 = a bounded wait gave up; bit 1 (decode only) = a decode sequence's
-// seq_start / seq_len were out of range.
+// bit 0 = a bounded wait gave up; bit 1 (decodes and commits) = a sequence's
+// device-side arguments were out of range.
 unsigned int read_and_clear_status_decode();
 unsigned int read_and_clear_status_prefill_tc();
 unsigned int read_and_clear_status_prefill_pair();
@@ -144,6 +204,8 @@ unsigned int read_and_clear_status_project_tc();
 unsigned int read_and_clear_status_linear();
 unsigned int read_and_clear_status_ring();
 unsigned int read_and_clear_status_step_proj();
+unsigned int read_and_clear_status_tree();
+unsigned int read_and_clear_status_commit();
 
 int device_sm_count();
 

@@ -1,0 +1,376 @@
+// Attention of drafted tokens over the shared cache or the self-decoder's ring
+// (sm_100a): the work plan, the CUDA-core kernel and the join of shared
+// streams.
+//
+// A decoder that drafts several tokens ahead checks them in one pass: node i of
+// a tree of up to 64 drafted tokens attends to the sequence's context and to
+// its own ancestors among the nodes.  The cross-decoder's context is the one
+// shared cache ("YOCO: Caching Once for Decoder-Decoder Long-Context Language
+// Models", podcast transcript, cue 26), the self-decoder's the window ring
+// ("You Only Cache Once", paperlayer summary, section 3 "Sliding-Window
+// Attention"); the pages do not draft.  With x_j = scale q k_j over the keys
+// that a row sees, m = max x, l = sum e^(x_j - m): o = sum e^(x_j - m) v_j / l,
+// lse = m + ln l, and o = 0, lse = -inf for a row that sees nothing.
+#include "tree.cuh"
+
+#include <algorithm>
+
+namespace yoco {
+
+// Bit 1: a sequence's arguments were out of range.
+static __device__ unsigned int g_status_tree;
+constexpr unsigned int kStatusBadSequence = 2u;
+
+namespace tree {
+namespace {
+
+constexpr int kSimtThreads = 256;
+constexpr int kSimtRows = 32;     // RS of the CUDA-core kernel
+constexpr int kSimtKeys = 64;     // BN of the CUDA-core kernel
+constexpr int kMergeWarps = 8;
+
+template <typename T>
+YOCO_DEV void load16(const T *src, float *f) {
+    Chunk<T>::unpack(*reinterpret_cast<const uint4 *>(src), f);
+}
+
+}  // namespace
+
+// CUDA-core kernel: 256 threads for 32 rows x 64 keys.  Thread (ty, tx) of a
+// 16 x 16 grid holds rows 2 ty, 2 ty + 1: in S = q K^T the keys tx, tx + 16,
+// tx + 32, tx + 48; in O += P V the columns 4 tx + 64 j.  A row's statistics
+// are the same in its 16 threads.  P of a key that the row does not see is -1
+// in shared memory, and the product leaves such a key out, so what its K and V
+// hold (infinities, NaN) never reaches the row.
+template <typename T, int D, bool RING>
+__global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const Params p) {
+    constexpr int RS = kSimtRows, BN = kSimtKeys, PITCH = D + 4, PP = BN + 4;
+    constexpr int EPC = Chunk<T>::N, NJ = D / 64;
+    extern __shared__ __align__(16) float smem[];
+    float *sq = smem, *sk = sq + RS * PITCH, *sv = sk + BN * PITCH, *sp = sv + BN * PITCH;
+    __shared__ Range s_range;
+    __shared__ uint64_t s_nodes[RS];
+    __shared__ int s_slot[BN];
+    __shared__ RingBounds s_bounds[RS];
+    pdl_trigger();
+    pdl_wait();
+    if (threadIdx.x < 32) {
+        const Range r = find_range<RING, RS, BN>(p);
+        if (threadIdx.x == 0) s_range = r;
+    }
+    __syncthreads();
+    const int G = p.Hq / p.Hkv;
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    SegIter<RING, RS, BN> it(p, s_range);
+    Seg g;
+    while (it.next(p, g)) {
+        const int rows = min(RS, g.n * G - g.rt * RS);
+        __syncthreads();
+        for (int c = tid; c < RS * (D / EPC); c += kSimtThreads) {
+            const int r = c / (D / EPC), d = (c % (D / EPC)) * EPC;
+            float f[EPC];
+#pragma unroll
+            for (int e = 0; e < EPC; ++e) f[e] = 0.f;
+            if (r < rows) {
+                const int rr = g.rt * RS + r;
+                load16(static_cast<const T *>(p.q) +
+                           (((int64_t)g.b * p.N + rr / G) * p.Hq + g.g * G + rr % G) * D + d, f);
+            }
+#pragma unroll
+            for (int e = 0; e < EPC; ++e) sq[r * PITCH + d + e] = f[e] * p.scale_log2;
+        }
+        if (tid < RS) {
+            const int i = (g.rt * RS + tid) / G;
+            s_nodes[tid] = tid < rows ? visible_nodes<RING>(p, g.b, g.n, i) : 0;
+            if (RING) {
+                if (tid < rows) s_bounds[tid] = ring_bounds(p.node_pos[(int64_t)g.b * p.N + i], p.window);
+                else s_bounds[tid] = RingBounds{-1, -1};
+            }
+        }
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[2][NJ * 4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < NJ * 4; ++e) o[i][e] = 0.f;
+
+        for (int t = g.t0; t < g.t1; ++t) {
+            const bool nodes = t == g.n_ctx_tiles;
+            const int64_t j0 = nodes ? 0 : (int64_t)t * BN;
+            const int cnt = nodes ? g.n : (int)sched::min64(BN, g.ctx - j0);
+            const int64_t row0 = nodes ? (int64_t)g.b * p.N : g.row0 + j0;
+            const T *kb = static_cast<const T *>(nodes ? p.k_nodes : p.k);
+            const T *vb = static_cast<const T *>(nodes ? p.v_nodes : p.v);
+            __syncthreads();
+            for (int c = tid; c < BN * (D / EPC); c += kSimtThreads) {
+                const int j = c / (D / EPC), d = (c % (D / EPC)) * EPC;
+                float fk[EPC], fv[EPC];
+#pragma unroll
+                for (int e = 0; e < EPC; ++e) fk[e] = fv[e] = 0.f;
+                if (j < cnt) {
+                    const int64_t off = ((row0 + j) * p.Hkv + g.g) * D + d;
+                    load16(kb + off, fk);
+                    load16(vb + off, fv);
+                }
+#pragma unroll
+                for (int e = 0; e < EPC; e += 4) {
+                    *reinterpret_cast<float4 *>(sk + j * PITCH + d + e) = make_float4(fk[e], fk[e + 1], fk[e + 2], fk[e + 3]);
+                    *reinterpret_cast<float4 *>(sv + j * PITCH + d + e) = make_float4(fv[e], fv[e + 1], fv[e + 2], fv[e + 3]);
+                }
+            }
+            if (RING && !nodes && tid < BN)
+                s_slot[tid] = tid < cnt ? p.slot_pos[(int64_t)g.b * p.window + j0 + tid] : -1;
+            __syncthreads();
+
+            float s[2][4] = {};
+#pragma unroll 4
+            for (int d = 0; d < D; d += 4) {
+                float4 a[2], bk[4];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) a[i] = *reinterpret_cast<const float4 *>(sq + (2 * ty + i) * PITCH + d);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) bk[j] = *reinterpret_cast<const float4 *>(sk + (tx + 16 * j) * PITCH + d);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        s[i][j] = fmaf(a[i].x, bk[j].x, s[i][j]);
+                        s[i][j] = fmaf(a[i].y, bk[j].y, s[i][j]);
+                        s[i][j] = fmaf(a[i].z, bk[j].z, s[i][j]);
+                        s[i][j] = fmaf(a[i].w, bk[j].w, s[i][j]);
+                    }
+            }
+            bool all = true;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                bool see[4];
+                float mx = m[i];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int c = tx + 16 * j;
+                    if (nodes) see[j] = (s_nodes[2 * ty + i] >> c) & 1;
+                    else if (RING) see[j] = c < cnt && s_bounds[2 * ty + i].sees(s_slot[c]);
+                    else see[j] = c < cnt;
+                    all &= see[j];
+                    // a NaN score has to reach the row: fmaxf would drop it, the exponential below does not
+                    if (see[j]) mx = fmaxf(mx, s[i][j]);
+                }
+#pragma unroll
+                for (int w = 8; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+                const float al = mx == -INFINITY ? 1.f : exp2f(m[i] - mx);
+                const float ref = mx == -INFINITY ? 0.f : mx;
+                m[i] = mx;
+                l[i] *= al;
+#pragma unroll
+                for (int e = 0; e < NJ * 4; ++e) o[i][e] *= al;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float e = exp2f(s[i][j] - ref);
+                    if (see[j]) l[i] += e;
+                    sp[(2 * ty + i) * PP + tx + 16 * j] = see[j] ? e : -1.f;
+                }
+            }
+            all = __all_sync(0xffffffffu, all);
+            __syncwarp();
+            if (all) {
+#pragma unroll 4
+                for (int c = 0; c < BN; ++c) {
+                    const float p0 = sp[(2 * ty) * PP + c], p1 = sp[(2 * ty + 1) * PP + c];
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j) {
+                        const float4 v = *reinterpret_cast<const float4 *>(sv + c * PITCH + 4 * tx + 64 * j);
+                        o[0][4 * j] = fmaf(p0, v.x, o[0][4 * j]);
+                        o[0][4 * j + 1] = fmaf(p0, v.y, o[0][4 * j + 1]);
+                        o[0][4 * j + 2] = fmaf(p0, v.z, o[0][4 * j + 2]);
+                        o[0][4 * j + 3] = fmaf(p0, v.w, o[0][4 * j + 3]);
+                        o[1][4 * j] = fmaf(p1, v.x, o[1][4 * j]);
+                        o[1][4 * j + 1] = fmaf(p1, v.y, o[1][4 * j + 1]);
+                        o[1][4 * j + 2] = fmaf(p1, v.z, o[1][4 * j + 2]);
+                        o[1][4 * j + 3] = fmaf(p1, v.w, o[1][4 * j + 3]);
+                    }
+                }
+            } else {
+                for (int c = 0; c < cnt; ++c) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float pp = sp[(2 * ty + i) * PP + c];
+                        if (pp < 0.f) continue;   // not seen (a NaN goes on)
+#pragma unroll
+                        for (int j = 0; j < NJ; ++j) {
+                            const float4 v = *reinterpret_cast<const float4 *>(sv + c * PITCH + 4 * tx + 64 * j);
+                            o[i][4 * j] = fmaf(pp, v.x, o[i][4 * j]);
+                            o[i][4 * j + 1] = fmaf(pp, v.y, o[i][4 * j + 1]);
+                            o[i][4 * j + 2] = fmaf(pp, v.z, o[i][4 * j + 2]);
+                            o[i][4 * j + 3] = fmaf(pp, v.w, o[i][4 * j + 3]);
+                        }
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float L = l[i];
+#pragma unroll
+            for (int w = 8; w > 0; w >>= 1) L += __shfl_xor_sync(0xffffffffu, L, w);
+            const int r = 2 * ty + i;
+            if (r >= rows) continue;
+            const int rr = g.rt * RS + r, node = rr / G, h = g.g * G + rr % G;
+            if (g.whole) {
+                const bool none = m[i] == -INFINITY && L == 0.f;   // a NaN sum is not nothing
+                const float inv = none ? 0.f : 1.f / L;
+                T *dst = static_cast<T *>(p.o) + (((int64_t)g.b * p.N + node) * p.Hq + h) * D;
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) dst[4 * tx + 64 * j + e] = from_f32<T>(o[i][4 * j + e] * inv);
+                if (p.lse && tx == 0)
+                    p.lse[((int64_t)g.b * p.Hq + h) * p.N + node] =
+                        none ? -INFINITY : (m[i] + log2f(L)) * kLn2;
+            } else {
+                const int64_t e = ((int64_t)blockIdx.x * 2 + g.slot) * RS + r;
+                if (tx == 0) p.ws_ml[e] = make_float2(m[i], L);
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)
+                    *reinterpret_cast<float4 *>(p.ws_o + e * D + 4 * tx + 64 * j) =
+                        make_float4(o[i][4 * j], o[i][4 * j + 1], o[i][4 * j + 2], o[i][4 * j + 3]);
+            }
+        }
+    }
+}
+
+// Joins the partials of shared streams, one warp per (sequence, node, query
+// head); also writes the rows without a node (and every row of a sequence out
+// of range, which it reports): o = 0, lse = -inf.  grid: the CTAs of the
+// kernel before it.
+template <typename T, int D, bool RING, int RS, int BN>
+__global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const Params p, const int n_cta) {
+    constexpr int DPL = D / 32;
+    const int lane = threadIdx.x & 31;
+    const int64_t row = (int64_t)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+    pdl_trigger();
+    pdl_wait();
+    if (row >= (int64_t)p.B * p.N * p.Hq) return;
+    const int h = (int)(row % p.Hq);
+    const int64_t bn = row / p.Hq;
+    const int node = (int)(bn % p.N), b = (int)(bn / p.N);
+    const int G = p.Hq / p.Hkv;
+    const Seq s = sequence<RING, RS, BN>(p, b);
+    T *dst = static_cast<T *>(p.o) + row * D + lane * DPL;
+    float *lse = p.lse ? p.lse + ((int64_t)b * p.Hq + h) * p.N + node : nullptr;
+    float M = -INFINITY, L = 0.f, acc[DPL];
+#pragma unroll
+    for (int e = 0; e < DPL; ++e) acc[e] = 0.f;
+    if (node < s.n) {
+        const int rr = node * G + h % G;
+        const int64_t T_all = p.prefix[p.B], grid = sched::min64(T_all, n_cta);
+        const int nt = s.n_ctx_tiles + 1;
+        const int64_t a = p.prefix[b] + (int64_t)((rr / RS) * p.Hkv + h / G) * nt;
+        const int64_t c0 = range_owner(T_all, a, grid), c1 = range_owner(T_all, a + nt - 1, grid);
+        if (c0 == c1) return;   // finished by its CTA
+        // the stream's part in c0 opens c0's range only when it starts there
+        const int64_t first = c0 * 2 + (range_start(T_all, c0, grid) == a ? 0 : 1);
+        const int n_part = (int)(c1 - c0) + 1;
+        auto entry = [&](int i) { return (i == 0 ? first : (c0 + i) * 2) * RS + rr % RS; };
+        for (int i = lane; i < n_part; i += 32) M = fmaxf(M, p.ws_ml[entry(i)].x);
+        M = warp_max(M);
+        const float ref = M == -INFINITY ? 0.f : M;
+        for (int i0 = 0; i0 < n_part; i0 += 32) {
+            float w = 0.f;
+            if (i0 + lane < n_part) {
+                const float2 ml = p.ws_ml[entry(i0 + lane)];
+                w = exp2f(ml.x - ref);
+                L += ml.y * w;
+            }
+            const int cnt = min(32, n_part - i0);
+#pragma unroll 4
+            for (int i = 0; i < cnt; ++i) {
+                const float wi = __shfl_sync(0xffffffffu, w, i);
+                const float *src = p.ws_o + entry(i0 + i) * D + lane * DPL;
+#pragma unroll
+                for (int e = 0; e < DPL; ++e) acc[e] = fmaf(wi, src[e], acc[e]);
+            }
+        }
+        L = warp_sum(L);
+    } else if (!s.ok && node == 0 && h == 0 && lane == 0) {
+        atomicOr(&g_status_tree, kStatusBadSequence);
+    }
+    const bool none = M == -INFINITY && L == 0.f;
+    const float inv = none ? 0.f : 1.f / L;
+#pragma unroll
+    for (int e = 0; e < DPL; ++e) dst[e] = from_f32<T>(acc[e] * inv);
+    if (lse && lane == 0) *lse = none ? -INFINITY : (M + log2f(L)) * kLn2;
+}
+
+// ------------------------------------------------------------------- host
+namespace {
+
+Params make_params(const TreeArgs &a, const TreePlan &pl) {
+    Params p;
+    p.q = a.q; p.k_nodes = a.k_nodes; p.v_nodes = a.v_nodes; p.k = a.k; p.v = a.v;
+    p.seq_start = a.seq_start; p.seq_len = a.seq_len; p.slot_pos = a.slot_pos; p.node_pos = a.node_pos;
+    p.mask = a.mask; p.n_nodes = a.n_nodes;
+    p.B = a.B; p.N = a.N; p.Hq = a.Hq; p.Hkv = a.Hkv; p.window = a.window;
+    p.cache_rows = a.cache_rows; p.max_len = a.max_len;
+    p.scale_log2 = a.scale * kLog2e;
+    p.o = a.o; p.lse = a.lse;
+    unsigned char *ws = static_cast<unsigned char *>(a.ws);
+    p.prefix = reinterpret_cast<int64_t *>(ws);
+    p.ws_ml = reinterpret_cast<float2 *>(ws + pl.ml_off);
+    p.ws_o = reinterpret_cast<float *>(ws + pl.o_off);
+    return p;
+}
+
+template <typename T, int D, bool RING>
+cudaError_t launch_simt(const TreeArgs &a, const TreePlan &pl, cudaStream_t st) {
+    const Params p = make_params(a, pl);
+    constexpr size_t smem = sizeof(float) * ((kSimtRows + 2 * kSimtKeys) * (D + 4) + kSimtRows * (kSimtKeys + 4));
+    auto kern = tree_simt_kernel<T, D, RING>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    note_launches(2);
+    e = launch_pdl(kern, dim3(pl.grid), dim3(kSimtThreads), smem, st, p);
+    if (e != cudaSuccess) return e;
+    const int64_t rows = (int64_t)a.B * a.N * a.Hq;
+    return launch_pdl(tree_merge_kernel<T, D, RING, kSimtRows, kSimtKeys>,
+                      dim3((unsigned)((rows + kMergeWarps - 1) / kMergeWarps)), dim3(32 * kMergeWarps), 0, st, p, pl.grid);
+}
+
+template <typename T>
+cudaError_t launch_simt_t(const TreeArgs &a, const TreePlan &pl, cudaStream_t st) {
+    if (a.D == 128) return a.window > 0 ? launch_simt<T, 128, true>(a, pl, st) : launch_simt<T, 128, false>(a, pl, st);
+    if (a.D == 64) return a.window > 0 ? launch_simt<T, 64, true>(a, pl, st) : launch_simt<T, 64, false>(a, pl, st);
+    return cudaErrorNotSupported;
+}
+
+}  // namespace
+}  // namespace tree
+
+bool make_tree_plan(int32_t B, int32_t N, int64_t max_len, int Hq, int Hkv, int D, int dtype, TreePlan *plan) {
+    TreePlan pl;
+    pl.rows = tree::kSimtRows;
+    pl.keys = tree::kSimtKeys;
+    // streams and tiles at full length: no CTA without a tile is launched
+    const int64_t streams = (int64_t)B * ((N * (Hq / Hkv) + pl.rows - 1) / pl.rows) * Hkv;
+    const int64_t tiles = streams * ((max_len + pl.keys - 1) / pl.keys + 1);
+    if ((int64_t)B * N * Hq > (int64_t)INT32_MAX || tiles > (INT64_MAX >> 16)) return false;
+    pl.grid = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, 2 * device_sm_count()));
+    pl.ml_off = ((size_t)(B + 1) * sizeof(int64_t) + 15) / 16 * 16;
+    const size_t entries = (size_t)pl.grid * 2 * pl.rows;
+    pl.o_off = pl.ml_off + entries * sizeof(float2);
+    pl.ws_bytes = pl.o_off + entries * D * sizeof(float);
+    *plan = pl;
+    return true;
+}
+
+cudaError_t launch_tree(const TreeArgs &a, const TreePlan &pl, cudaStream_t st) {
+    if (a.dtype == kBF16) return tree::launch_simt_t<__nv_bfloat16>(a, pl, st);
+    return tree::launch_simt_t<float>(a, pl, st);
+}
+
+unsigned int read_and_clear_status_tree() {
+    unsigned int h = 0, z = 0;
+    if (cudaMemcpyFromSymbol(&h, g_status_tree, sizeof(h)) != cudaSuccess) return 0;
+    cudaMemcpyToSymbol(g_status_tree, &z, sizeof(z));
+    return h;
+}
+
+}  // namespace yoco

@@ -1,0 +1,163 @@
+"""Argument checks and host helpers of the rotary positions and the drafted-token
+calls, without a GPU."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import shared_kv_decoder_b200 as yoco
+from tests import tree_ref as tr
+
+FAKE = ctypes.c_void_p(0x10000)   # 16-byte aligned, never dereferenced: validation fails first
+OTHER = ctypes.c_void_p(0x20000)
+MISALIGNED = ctypes.c_void_p(0x10008)
+
+
+def _cfg(Hq=32, Hkv=8, D=128, dtype=0, scale=0.0):
+    return ctypes.byref(yoco.AttnCfg(Hq, Hkv, D, scale, dtype))
+
+
+@pytest.mark.parametrize("rot", [16, 48, 64, 128])
+@pytest.mark.parametrize("theta", [10000.0, 640000.0])
+@pytest.mark.parametrize("sc", [dict(), dict(scaling="linear", factor=3.0), dict(scaling="ntk", factor=8.0),
+                                dict(scaling="by_parts", factor=16.0, orig_len=4096),
+                                dict(scaling="by_parts", factor=8.0, orig_len=8192, beta_fast=4.0, beta_slow=0.5)])
+def test_rope_config(rot, theta, sc):
+    cfg = yoco.rope_config(rot, theta=theta, layout="interleaved", **sc)
+    ref = {{"beta_fast": "fast", "beta_slow": "slow"}.get(k, k): v for k, v in sc.items()}
+    w, m = tr.inv_freq(rot, theta, **ref)
+    assert cfg.rot_dim == rot and cfg.layout == 1
+    # pow within an ulp or two and five more operations in 64 bits
+    np.testing.assert_allclose(np.array(cfg.inv_freq)[:rot // 2], w, rtol=16 * 2.0 ** -53)
+    assert not np.array(cfg.inv_freq)[rot // 2:].any()
+    assert abs(cfg.mscale - m) <= 4 * 2.0 ** -53 * m
+    assert yoco.rope_config(rot, mscale=0.5, **sc).mscale == 0.5
+
+
+@pytest.mark.parametrize("bad", [dict(rot_dim=8), dict(rot_dim=40), dict(rot_dim=144), dict(theta=0.0),
+                                 dict(theta=float("inf")), dict(theta=float("nan")), dict(scaling="linear", factor=0.5),
+                                 dict(scaling="ntk", factor=float("nan")), dict(scaling="by_parts", factor=2.0),
+                                 dict(scaling="by_parts", factor=2.0, orig_len=64, beta_fast=1.0), dict(mscale=-1.0)])
+def test_rope_config_refusals(bad):
+    with pytest.raises(yoco.YocoError) as e:
+        yoco.rope_config(**{"rot_dim": 64, **bad})
+    assert e.value.status == yoco.ERR_INVALID
+
+
+def test_rope_config_names():
+    with pytest.raises(ValueError):
+        yoco.rope_config(64, layout="neox")
+    with pytest.raises(ValueError):
+        yoco.rope_config(64, scaling="yarn")
+
+
+def test_rope_arguments_rejected_before_launch():
+    L = yoco.load()
+    good = yoco.rope_config(64)
+
+    def call(q=FAKE, k=FAKE, B=2, T=3, pos=None, qo=FAKE, ko=FAKE, rope=good, cfg=_cfg()):
+        return L.yoco_rope(q, k, B, T, pos, 0, 0, qo, ko, ctypes.byref(rope) if rope is not None else None, cfg, None)
+    assert call(rope=None) == yoco.ERR_INVALID
+    assert call(cfg=None) == yoco.ERR_INVALID
+    assert call(cfg=_cfg(D=96)) == yoco.ERR_UNSUPPORTED
+    assert call(q=None, k=None, qo=None, ko=None) == yoco.ERR_INVALID
+    assert call(q=None) == yoco.ERR_INVALID                # an output without its input
+    assert call(ko=None) == yoco.ERR_INVALID
+    assert call(q=MISALIGNED) == yoco.ERR_INVALID
+    assert call(ko=MISALIGNED) == yoco.ERR_INVALID
+    assert call(pos=MISALIGNED) == yoco.ERR_INVALID
+    assert call(B=-1) == yoco.ERR_INVALID
+    assert call(T=-1) == yoco.ERR_INVALID
+    assert call(B=2, T=1 << 62) == yoco.ERR_INVALID
+    assert call(rope=yoco.rope_config(128), cfg=_cfg(D=64)) == yoco.ERR_UNSUPPORTED
+    for field, value in [("rot_dim", 8), ("rot_dim", 72), ("layout", 2), ("mscale", float("nan"))]:
+        r = yoco.rope_config(64)
+        setattr(r, field, value)
+        assert call(rope=r) == yoco.ERR_INVALID
+    r = yoco.rope_config(64)
+    r.inv_freq[31] = float("inf")
+    assert call(rope=r) == yoco.ERR_INVALID
+    assert call(B=0) == yoco.OK and call(T=0) == yoco.OK
+
+
+def test_cross_decode_tree_arguments_rejected_before_launch():
+    L = yoco.load()
+    B, N, M, R = 4, 16, 4096, 1 << 20
+    need = L.yoco_cross_decode_tree_workspace_size(B, N, M, _cfg())
+    assert need > 0
+
+    def call(q=FAKE, kn=FAKE, kc=FAKE, rows=R, ss=FAKE, sl=FAKE, mask=None, nn=None, b=B, n=N, m=M, o=FAKE, lse=None,
+             ws=FAKE, wsb=need, cfg=_cfg()):
+        return L.yoco_cross_decode_tree(q, kn, FAKE, kc, FAKE, rows, ss, sl, mask, nn, b, n, m, o, lse, ws, wsb, cfg, None)
+    for bad in [dict(q=None), dict(kn=None), dict(kc=MISALIGNED), dict(ss=None), dict(sl=None), dict(mask=MISALIGNED),
+                dict(nn=MISALIGNED), dict(o=None), dict(lse=MISALIGNED), dict(rows=0), dict(rows=1 << 31), dict(b=-1),
+                dict(n=0), dict(m=-1), dict(m=1 << 31), dict(cfg=_cfg(Hq=30)), dict(cfg=_cfg(dtype=5))]:
+        assert call(**bad) == yoco.ERR_INVALID, bad
+    for bad in [dict(n=65), dict(cfg=_cfg(D=96)), dict(cfg=_cfg(Hq=48, Hkv=3))]:
+        assert call(**bad) == yoco.ERR_UNSUPPORTED, bad
+    for bad in [dict(ws=None), dict(ws=MISALIGNED), dict(wsb=need - 1)]:
+        assert call(**bad) == yoco.ERR_WORKSPACE, bad
+    assert call(b=0) == yoco.OK
+
+
+def test_swa_decode_tree_arguments_rejected_before_launch():
+    L = yoco.load()
+    B, N, W = 4, 16, 1024
+    need = L.yoco_swa_decode_tree_workspace_size(B, N, W, _cfg())
+    assert need == L.yoco_cross_decode_tree_workspace_size(B, N, W, _cfg())
+
+    def call(q=FAKE, pos=FAKE, mask=None, nn=None, b=B, n=N, w=W, rk=FAKE, sp=FAKE, o=FAKE, lse=None, ws=FAKE, wsb=need,
+             cfg=_cfg()):
+        return L.yoco_swa_decode_tree(q, FAKE, FAKE, pos, mask, nn, b, n, w, rk, FAKE, sp, o, lse, ws, wsb, cfg, None)
+    for bad in [dict(q=None), dict(pos=None), dict(pos=MISALIGNED), dict(mask=MISALIGNED), dict(nn=MISALIGNED),
+                dict(rk=None), dict(sp=None), dict(o=MISALIGNED), dict(lse=MISALIGNED), dict(b=-1), dict(n=0), dict(w=0)]:
+        assert call(**bad) == yoco.ERR_INVALID, bad
+    assert call(n=65) == yoco.ERR_UNSUPPORTED
+    for bad in [dict(ws=None), dict(ws=MISALIGNED), dict(wsb=need - 1)]:
+        assert call(**bad) == yoco.ERR_WORKSPACE, bad
+    assert call(b=0) == yoco.OK
+
+
+def test_commit_arguments_rejected_before_launch():
+    L = yoco.load()
+
+    def cross(kn=FAKE, path=FAKE, np_=FAKE, b=2, n=8, kc=FAKE, rows=100, ss=FAKE, sl=FAKE, cap=None, nl=OTHER, cfg=_cfg()):
+        return L.yoco_cross_tree_commit(kn, FAKE, path, np_, b, n, kc, FAKE, rows, ss, sl, cap, nl, cfg, None)
+    for bad in [dict(kn=None), dict(path=None), dict(np_=MISALIGNED), dict(b=-1), dict(n=0), dict(kc=None), dict(rows=0),
+                dict(rows=1 << 31), dict(ss=None), dict(sl=None), dict(cap=MISALIGNED), dict(nl=None), dict(nl=FAKE),
+                dict(cfg=None)]:
+        assert cross(**bad) == yoco.ERR_INVALID, bad
+    assert cross(n=65) == yoco.ERR_UNSUPPORTED
+    assert cross(b=0) == yoco.OK
+
+    def swa(kn=FAKE, pos=FAKE, path=FAKE, np_=FAKE, b=2, n=8, w=32, rk=FAKE, sp=FAKE, cfg=_cfg()):
+        return L.yoco_swa_tree_commit(kn, FAKE, pos, path, np_, b, n, w, rk, FAKE, sp, cfg, None)
+    for bad in [dict(kn=MISALIGNED), dict(pos=None), dict(path=None), dict(np_=None), dict(b=-1), dict(n=0), dict(w=0),
+                dict(rk=None), dict(sp=None), dict(cfg=_cfg(Hq=30))]:
+        assert swa(**bad) == yoco.ERR_INVALID, bad
+    assert swa(n=65) == yoco.ERR_UNSUPPORTED
+    assert swa(b=0) == yoco.OK
+
+
+def test_workspace_sizes():
+    sizes = [yoco.cross_decode_tree_workspace_size(B, N, M, 32, 8, 128, torch.bfloat16)
+             for B, N, M in [(1, 1, 0), (1, 1, 64), (1, 16, 4096), (16, 64, 131072)]]
+    assert all(s > 0 for s in sizes) and sizes == sorted(sizes)
+    for bad in [(0, 1, 64), (1, 0, 64), (1, 65, 64), (1, 1, -1)]:
+        assert yoco.cross_decode_tree_workspace_size(*bad, 32, 8, 128, torch.bfloat16) == 0
+    assert yoco.swa_decode_tree_workspace_size(1, 1, 0, 32, 8, 128, torch.bfloat16) == 0
+
+
+def test_cpu_tensors_are_refused():
+    q, k = torch.zeros(1, 2, 4, 64), torch.zeros(1, 2, 2, 64)
+    with pytest.raises(ValueError):
+        yoco.rope(q, k, yoco.rope_config(64))
+    with pytest.raises(ValueError):
+        yoco.cross_decode_tree(q, k, k, k[0], k[0], None, None, 1)
+    with pytest.raises(ValueError):
+        yoco.swa_decode_tree(q, k, k, None, None, None, None, 8)
+    with pytest.raises(ValueError):
+        yoco.cross_tree_commit(k, k, None, None, None, None, None, None)
+    with pytest.raises(ValueError):
+        yoco.swa_tree_commit(k, k, None, None, None, None, None, None, 8)
