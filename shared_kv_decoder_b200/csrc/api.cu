@@ -655,7 +655,8 @@ yoco_status yoco_get_device_status(cudaStream_t stream) {
                            read_and_clear_status_prefill_pair() | read_and_clear_status_project_tc() |
                            read_and_clear_status_gret_tc() | read_and_clear_status_linear() |
                            read_and_clear_status_ring() | read_and_clear_status_step_proj() |
-                           read_and_clear_status_tree() | read_and_clear_status_commit();
+                           read_and_clear_status_tree() | read_and_clear_status_tree_tc() |
+                           read_and_clear_status_commit();
     if (s & 1u) return YOCO_ERR_TIMEOUT;
     if (s & 2u) return YOCO_ERR_INVALID;
     return e == cudaSuccess ? YOCO_OK : YOCO_ERR_CUDA;

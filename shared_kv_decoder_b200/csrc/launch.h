@@ -173,6 +173,8 @@ struct TreeArgs {
     void *ws;
 };
 cudaError_t launch_tree(const TreeArgs &a, const TreePlan &plan, cudaStream_t s);
+// Its tensor-core kernel (bf16), without the join.
+cudaError_t launch_tree_tc(const TreeArgs &a, const TreePlan &plan, cudaStream_t s);
 
 struct CommitArgs {
     const void *k_nodes, *v_nodes;  // [B, N, row]
@@ -205,6 +207,7 @@ unsigned int read_and_clear_status_linear();
 unsigned int read_and_clear_status_ring();
 unsigned int read_and_clear_status_step_proj();
 unsigned int read_and_clear_status_tree();
+unsigned int read_and_clear_status_tree_tc();
 unsigned int read_and_clear_status_commit();
 
 int device_sm_count();

@@ -83,7 +83,6 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     const int stride = gridDim.y * kRopeThreads;
     for (int base = blockIdx.y * kRopeThreads + threadIdx.x; base < total; base += kUnroll * stride) {
         uint4 x0[kUnroll], x1[kUnroll];
-        int64_t dst[kUnroll];
         int at[kUnroll];   // the unit's first entry of s_cs, or -1: copied
         int gap[kUnroll];
         T *out[kUnroll];

@@ -303,42 +303,35 @@ __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const Para
 // ------------------------------------------------------------------- host
 namespace {
 
-Params make_params(const TreeArgs &a, const TreePlan &pl) {
-    Params p;
-    p.q = a.q; p.k_nodes = a.k_nodes; p.v_nodes = a.v_nodes; p.k = a.k; p.v = a.v;
-    p.seq_start = a.seq_start; p.seq_len = a.seq_len; p.slot_pos = a.slot_pos; p.node_pos = a.node_pos;
-    p.mask = a.mask; p.n_nodes = a.n_nodes;
-    p.B = a.B; p.N = a.N; p.Hq = a.Hq; p.Hkv = a.Hkv; p.window = a.window;
-    p.cache_rows = a.cache_rows; p.max_len = a.max_len;
-    p.scale_log2 = a.scale * kLog2e;
-    p.o = a.o; p.lse = a.lse;
-    unsigned char *ws = static_cast<unsigned char *>(a.ws);
-    p.prefix = reinterpret_cast<int64_t *>(ws);
-    p.ws_ml = reinterpret_cast<float2 *>(ws + pl.ml_off);
-    p.ws_o = reinterpret_cast<float *>(ws + pl.o_off);
-    return p;
-}
-
 template <typename T, int D, bool RING>
 cudaError_t launch_simt(const TreeArgs &a, const TreePlan &pl, cudaStream_t st) {
-    const Params p = make_params(a, pl);
     constexpr size_t smem = sizeof(float) * ((kSimtRows + 2 * kSimtKeys) * (D + 4) + kSimtRows * (kSimtKeys + 4));
     auto kern = tree_simt_kernel<T, D, RING>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    note_launches(2);
-    e = launch_pdl(kern, dim3(pl.grid), dim3(kSimtThreads), smem, st, p);
-    if (e != cudaSuccess) return e;
-    const int64_t rows = (int64_t)a.B * a.N * a.Hq;
-    return launch_pdl(tree_merge_kernel<T, D, RING, kSimtRows, kSimtKeys>,
-                      dim3((unsigned)((rows + kMergeWarps - 1) / kMergeWarps)), dim3(32 * kMergeWarps), 0, st, p, pl.grid);
+    note_launches(1);
+    return launch_pdl(kern, dim3(pl.grid), dim3(kSimtThreads), smem, st, make_params(a, pl));
 }
 
-template <typename T>
-cudaError_t launch_simt_t(const TreeArgs &a, const TreePlan &pl, cudaStream_t st) {
-    if (a.D == 128) return a.window > 0 ? launch_simt<T, 128, true>(a, pl, st) : launch_simt<T, 128, false>(a, pl, st);
-    if (a.D == 64) return a.window > 0 ? launch_simt<T, 64, true>(a, pl, st) : launch_simt<T, 64, false>(a, pl, st);
-    return cudaErrorNotSupported;
+template <typename T, int D, bool RING, int RS, int BN>
+cudaError_t launch_merge(const TreeArgs &a, const TreePlan &pl, cudaStream_t st) {
+    const int64_t rows = (int64_t)a.B * a.N * a.Hq;
+    note_launches(1);
+    return launch_pdl(tree_merge_kernel<T, D, RING, RS, BN>, dim3((unsigned)((rows + kMergeWarps - 1) / kMergeWarps)),
+                      dim3(32 * kMergeWarps), 0, st, make_params(a, pl), pl.grid);
+}
+
+template <int D, bool RING>
+cudaError_t launch_d(const TreeArgs &a, const TreePlan &pl, cudaStream_t st) {
+    if (a.dtype == kBF16) {
+        const cudaError_t e = launch_tree_tc(a, pl, st);
+        if (e != cudaSuccess) return e;
+        return pl.rows == 128 ? launch_merge<__nv_bfloat16, D, RING, 128, kTcKeys>(a, pl, st)
+                              : launch_merge<__nv_bfloat16, D, RING, 256, kTcKeys>(a, pl, st);
+    }
+    const cudaError_t e = launch_simt<float, D, RING>(a, pl, st);
+    if (e != cudaSuccess) return e;
+    return launch_merge<float, D, RING, kSimtRows, kSimtKeys>(a, pl, st);
 }
 
 }  // namespace
@@ -346,13 +339,15 @@ cudaError_t launch_simt_t(const TreeArgs &a, const TreePlan &pl, cudaStream_t st
 
 bool make_tree_plan(int32_t B, int32_t N, int64_t max_len, int Hq, int Hkv, int D, int dtype, TreePlan *plan) {
     TreePlan pl;
-    pl.rows = tree::kSimtRows;
-    pl.keys = tree::kSimtKeys;
+    // bf16: the tensor-core kernel, one row tile of 128 or two; fp32: CUDA cores
+    pl.rows = dtype != kBF16 ? tree::kSimtRows : N * (Hq / Hkv) <= 128 ? 128 : 256;
+    pl.keys = dtype != kBF16 ? tree::kSimtKeys : tree::kTcKeys;
     // streams and tiles at full length: no CTA without a tile is launched
     const int64_t streams = (int64_t)B * ((N * (Hq / Hkv) + pl.rows - 1) / pl.rows) * Hkv;
     const int64_t tiles = streams * ((max_len + pl.keys - 1) / pl.keys + 1);
     if ((int64_t)B * N * Hq > (int64_t)INT32_MAX || tiles > (INT64_MAX >> 16)) return false;
-    pl.grid = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, 2 * device_sm_count()));
+    const int per_sm = dtype != kBF16 ? 2 : 1;
+    pl.grid = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, (int64_t)per_sm * device_sm_count()));
     pl.ml_off = ((size_t)(B + 1) * sizeof(int64_t) + 15) / 16 * 16;
     const size_t entries = (size_t)pl.grid * 2 * pl.rows;
     pl.o_off = pl.ml_off + entries * sizeof(float2);
@@ -362,8 +357,9 @@ bool make_tree_plan(int32_t B, int32_t N, int64_t max_len, int Hq, int Hkv, int 
 }
 
 cudaError_t launch_tree(const TreeArgs &a, const TreePlan &pl, cudaStream_t st) {
-    if (a.dtype == kBF16) return tree::launch_simt_t<__nv_bfloat16>(a, pl, st);
-    return tree::launch_simt_t<float>(a, pl, st);
+    if (a.D == 128) return a.window > 0 ? tree::launch_d<128, true>(a, pl, st) : tree::launch_d<128, false>(a, pl, st);
+    if (a.D == 64) return a.window > 0 ? tree::launch_d<64, true>(a, pl, st) : tree::launch_d<64, false>(a, pl, st);
+    return cudaErrorNotSupported;
 }
 
 unsigned int read_and_clear_status_tree() {

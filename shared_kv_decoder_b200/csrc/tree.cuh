@@ -24,6 +24,8 @@
 namespace yoco {
 namespace tree {
 
+constexpr int kTcKeys = 128;   // keys of a tile of the tensor-core kernel
+
 struct Params {
     const void *q, *k_nodes, *v_nodes;   // [B, N, Hq, D], [B, N, Hkv, D]
     const void *k, *v;                   // cache [cache_rows, Hkv, D] or ring [B, window, Hkv, D]
@@ -202,6 +204,22 @@ YOCO_DEV RingBounds ring_bounds(int64_t pos, int32_t window) {
     if (pos <= 0) return {-1, -1};
     const int64_t lo = sched::max64(pos - window, -1), hi = sched::min64(pos - 1, INT32_MAX);
     return {(int)sched::min64(lo, INT32_MAX), (int)hi};
+}
+
+inline Params make_params(const TreeArgs &a, const TreePlan &pl) {
+    Params p;
+    p.q = a.q; p.k_nodes = a.k_nodes; p.v_nodes = a.v_nodes; p.k = a.k; p.v = a.v;
+    p.seq_start = a.seq_start; p.seq_len = a.seq_len; p.slot_pos = a.slot_pos; p.node_pos = a.node_pos;
+    p.mask = a.mask; p.n_nodes = a.n_nodes;
+    p.B = a.B; p.N = a.N; p.Hq = a.Hq; p.Hkv = a.Hkv; p.window = a.window;
+    p.cache_rows = a.cache_rows; p.max_len = a.max_len;
+    p.scale_log2 = a.scale * kLog2e;
+    p.o = a.o; p.lse = a.lse;
+    unsigned char *ws = static_cast<unsigned char *>(a.ws);
+    p.prefix = reinterpret_cast<int64_t *>(ws);
+    p.ws_ml = reinterpret_cast<float2 *>(ws + pl.ml_off);
+    p.ws_o = reinterpret_cast<float *>(ws + pl.o_off);
+    return p;
 }
 
 }  // namespace tree

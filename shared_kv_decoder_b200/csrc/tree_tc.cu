@@ -1,0 +1,693 @@
+// Attention of drafted tokens on the sm_100a tensor cores (bf16 in, fp32
+// softmax and accumulation): the work of tree.cuh with 128-key tiles.
+//
+// The rows of one KV head -- every node's query heads of that group, row =
+// node * G + head -- are the M rows of S = Q K^T and O += P V, so one read of
+// the context serves all drafted tokens.  Two layouts:
+//   ALT   N * G <= 128: one 128-row tile, and the stream's KV tiles alternate
+//         between two softmax warpgroups, each with its own S / P and O and its
+//         own running maximum; they are added up when the segment ends.
+//   PAIR  more rows: two row tiles (256 rows) read the same KV tile.
+// Either way two softmax chains interleave on every SM sub-partition while the
+// tensor core works for the other one.  What bounds it: with R rows of a KV
+// head a 64 KB K / V tile (D = 128) takes 4 * 128 * max(R, 128) * 128 tensor
+// operations; at the measured rates the cache read is the longer one up to about
+// R = 250.
+//
+// Warp roles (320 threads), as in the prefill:
+//   warps 0-3, 4-7  softmax chains A and B: thread r owns row r (TMEM lane r)
+//   warp 8          TMA: lane 0 Q, lane 1 K, lane 2 V
+//   warp 9          MMA issue (one thread)
+// TMEM (512 columns): S_A/P_A, S_B/P_B, O_A, O_B, 128 columns each; P is bf16
+// over the first 64 columns of its S.
+//
+// Masks.  Only a tile that some row does not see whole is masked, by one bit a
+// column.  The product with V needs more: a weight of 0 times an infinity is
+// NaN, so in such a tile the V rows that no row sees are cleared in shared
+// memory before P V, and so are the infinities and NaN of rows that some row
+// may see -- those are then added to the outputs of the rows that do see them
+// when the segment ends (a path that finite inputs never take).
+//
+// Every mbarrier wait is bounded; a wait that gives up sets the status word,
+// and all roles fall through to the common exit, which waits for issued copies
+// and MMAs before freeing TMEM.
+#include <cuda.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "common.cuh"
+#include "launch.h"
+#include "tc.cuh"
+#include "tree.cuh"
+
+namespace yoco {
+
+static __device__ unsigned int g_status_tree_tc;
+
+namespace tree {
+namespace {
+
+constexpr int BN = kTcKeys;
+constexpr int kThreads = 320;
+constexpr int kTmemCols = 512;
+constexpr uint32_t kBlk = 128 * 128;   // one [128 rows x 128 bytes] swizzled block
+
+template <int D, bool PAIR>
+struct Smem {
+    static constexpr int KB = D / 64;
+    static constexpr uint32_t TILE = (uint32_t)KB * kBlk;
+    static constexpr int QTILES = PAIR ? 2 : 1;
+    static constexpr int KST = D == 128 ? 3 : 6;
+    static constexpr int VST = (D == 128 ? 3 : 6) - (PAIR ? 1 : 0);
+    static constexpr uint32_t Q = 0;
+    static constexpr uint32_t K = Q + QTILES * TILE;
+    static constexpr uint32_t V = K + KST * TILE;
+    static constexpr uint32_t ML = V + VST * TILE;      // float2[128]: chain B's (m, l)
+    static constexpr uint32_t BAR = ML + 128 * 8;
+    static constexpr uint32_t MISC = BAR + 40 * 8;
+    static constexpr uint32_t BYTES = MISC + 128;
+    static constexpr uint32_t ALLOC = BYTES + 1024;     // alignment slack
+};
+static_assert(Smem<128, true>::ALLOC <= 232448 && Smem<128, false>::ALLOC <= 232448, "shared memory");
+
+enum Bar {
+    kQFull = 0,    // 2: Q tile loaded
+    kQEmpty = 2,   // 2: last S MMA on the Q tile done
+    kSFull = 4,    // 2: S of chain A / B ready
+    kPFull = 6,    // 2: P written (128 arrivals)
+    kODone = 8,    // 2: P.V finished
+    kOFree = 10,   // 2: O read out (128 arrivals)
+    kML = 12,      // chain B's (m, l) written (128 arrivals)
+    kDrain = 13,
+    kKFull = 14,   // up to 6 each
+    kKEmpty = 20,
+    kVFull = 26,
+    kVEmpty = 32,
+    kNumBars = 38
+};
+
+struct Misc {
+    uint32_t tmem;
+    int abort;
+    int poison[4];   // by segment mod 4: the last segment with an infinity or NaN cleared from a seen V row
+    Range range;
+};
+static_assert(sizeof(Misc) <= 128, "misc area");
+
+YOCO_DEV bool wait1(uint64_t *bar, uint32_t parity) { return mbar_wait(bar, parity, &g_status_tree_tc); }
+YOCO_DEV bool waitw(uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, &g_status_tree_tc));
+}
+
+// Does a pair of bf16 hold an infinity or NaN (an exponent of all ones)?
+YOCO_DEV bool odd_pair(uint32_t w) { return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u; }
+YOCO_DEV uint32_t clear_odd(uint32_t w) {
+    if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+    if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
+    return w;
+}
+
+// Key row r of a V tile: cleared whole (unseen), or of its infinities and NaN;
+// true when there were any of those.
+template <int KB>
+YOCO_DEV bool clean_v_row(uint8_t *tile, int r, bool unseen) {
+    bool odd = false;
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            // by the swizzle's order, which keeps a quarter-warp off one bank group
+            uint4 *at = reinterpret_cast<uint4 *>(tile + kb * kBlk + r * 128 + ((c ^ (r & 7)) << 4));
+            if (unseen) {
+                *at = make_uint4(0, 0, 0, 0);
+                continue;
+            }
+            const uint4 v = *at;
+            if (odd_pair(v.x) || odd_pair(v.y) || odd_pair(v.z) || odd_pair(v.w)) {
+                odd = true;
+                *at = make_uint4(clear_odd(v.x), clear_odd(v.y), clear_odd(v.z), clear_odd(v.w));
+            }
+        }
+    return odd;
+}
+
+// The infinities and NaN of one seen V row, added to 32 columns of its output.
+YOCO_DEV void add_odd(const __nv_bfloat16 *v, float *o) {
+#pragma unroll
+    for (int e = 0; e < 32; e += 8) {
+        float f[8];
+        Chunk<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4 *>(v + e), f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (!isfinite(f[i])) o[e + i] += f[i];
+    }
+}
+
+// A ring segment's bounds over all its nodes: what every node sees and what
+// any does.
+struct RingSpan {
+    RingBounds every, any;
+};
+
+}  // namespace
+
+template <int D, bool RING, bool PAIR>
+__global__ void __launch_bounds__(kThreads, 1)
+    tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kn,
+                   const __grid_constant__ CUtensorMap tm_vn, const __grid_constant__ Params p) {
+    using L = Smem<D, PAIR>;
+    constexpr int KB = L::KB;
+    constexpr int RS = PAIR ? 256 : 128;
+    using Iter = SegIter<RING, RS, BN>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *sbase = smem_raw + (base - raw);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sbase + L::BAR);
+    Misc *misc = reinterpret_cast<Misc *>(sbase + L::MISC);
+    volatile int *abort_flag = &misc->abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int G = p.Hq / p.Hkv;
+
+    pdl_trigger();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&bars[kQFull + s], 1);
+            mbar_init(&bars[kQEmpty + s], 1);
+            mbar_init(&bars[kSFull + s], 1);
+            mbar_init(&bars[kPFull + s], 128);
+            mbar_init(&bars[kODone + s], 1);
+            mbar_init(&bars[kOFree + s], 128);
+        }
+        mbar_init(&bars[kML], 128);
+        mbar_init(&bars[kDrain], 1);
+        for (int s = 0; s < 6; ++s) {
+            mbar_init(&bars[kKFull + s], 1);
+            mbar_init(&bars[kKEmpty + s], 1);
+            mbar_init(&bars[kVFull + s], 1);
+            mbar_init(&bars[kVEmpty + s], 1);
+        }
+        misc->abort = 0;
+        for (int s = 0; s < 4; ++s) misc->poison[s] = -1;
+        fence_mbar_init();
+    }
+    if (warp == 9) {
+        tc::tmem_alloc(&misc->tmem, kTmemCols);
+        tc::tmem_relinquish();
+    }
+    pdl_wait();
+    if (warp == 8) {
+        const Range r = find_range<RING, RS, BN>(p);
+        if (lane == 0) {
+            misc->range = r;
+            // once any CTA has recorded a timeout, the rest of the grid does nothing
+            if (*(volatile unsigned int *)&g_status_tree_tc) misc->range.x = misc->range.end;
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = misc->tmem;
+    Iter it(p, misc->range);
+    Seg sg;
+
+    if (warp == 8) {
+        // ------------------------------------------------------ TMA producer
+        if (lane == 0) {
+            int k = 0;
+            for (; !*abort_flag && it.next(p, sg); ++k) {
+                bool ok = true;
+                for (int hh = 0; hh < L::QTILES; ++hh) {
+                    if (!wait1(&bars[kQEmpty + hh], (k & 1) ^ 1)) { ok = false; break; }
+                    mbar_arrive_expect_tx(&bars[kQFull + hh], 128 * D * 2);
+                    const int node0 = (sg.rt * L::QTILES + hh) * (128 / G);
+                    for (int kb = 0; kb < KB; ++kb)
+                        tc::tma_load_4d(base + L::Q + hh * L::TILE + kb * kBlk, &tm_q, kb * 64, sg.g * G, node0, sg.b,
+                                        &bars[kQFull + hh]);
+                }
+                if (!ok) { *abort_flag = 1; ++k; break; }
+            }
+            // drain: the last copies issued must land before this CTA may exit
+            if (k > 0)
+                for (int hh = 0; hh < L::QTILES; ++hh)
+                    if (!wait1(&bars[kQFull + hh], (k - 1) & 1)) break;
+        } else if (lane == 1 || lane == 2) {
+            const bool is_k = lane == 1;
+            const int ST = is_k ? L::KST : L::VST;
+            uint64_t *full = &bars[is_k ? kKFull : kVFull], *empty = &bars[is_k ? kKEmpty : kVEmpty];
+            const CUtensorMap *ctx_map = is_k ? &tm_k : &tm_v, *node_map = is_k ? &tm_kn : &tm_vn;
+            const uint32_t dst0 = base + (is_k ? L::K : L::V);
+            int u = 0;
+            while (!*abort_flag && it.next(p, sg)) {
+                for (int t = sg.t0; t < sg.t1; ++t, ++u) {
+                    const int st = u % ST;
+                    if (!wait1(&empty[st], ((u / ST) & 1) ^ 1)) { *abort_flag = 1; break; }
+                    if (*abort_flag) break;
+                    const bool nodes = t == sg.n_ctx_tiles;
+                    const int row = nodes ? 0 : RING ? t * BN : (int)(sg.row0 + (int64_t)t * BN);
+                    const int b = nodes || RING ? sg.b : 0;
+                    mbar_arrive_expect_tx(&full[st], (nodes ? kTreeMaxNodes : BN) * D * 2);
+                    for (int kb = 0; kb < KB; ++kb)
+                        tc::tma_load_4d(dst0 + st * L::TILE + kb * kBlk, nodes ? node_map : ctx_map, kb * 64, sg.g, row, b,
+                                        &full[st]);
+                }
+            }
+            for (int q = max(0, u - ST); q < u; ++q)
+                if (!wait1(&full[q % ST], (q / ST) & 1)) break;
+        }
+    } else if (warp == 9) {
+        // ---------------------------------------------------------- MMA issue
+        if (lane == 0) {
+            constexpr uint32_t idS = tc::idesc_bf16(128, BN, false, false);
+            constexpr uint32_t idPV = tc::idesc_bf16(128, D, false, true);
+            // the tile whose P.V is still owed to each chain: its tile counters
+            // (the CTA's, the chain's), its segment counters, and whether it
+            // opens its segment / holds the nodes
+            struct Owed {
+                int u, g, seg, k;
+                bool first, nodes;
+            } owed[2];
+            owed[0].u = owed[1].u = -1;
+            auto issue_pv = [&](int hh) -> bool {
+                Owed &w = owed[hh];
+                const int vs = w.u % L::VST;
+                if (w.first && w.k >= 1 && !wait1(&bars[kOFree + hh], (w.k - 1) & 1)) return false;
+                if (!wait1(&bars[kPFull + hh], w.g & 1)) return false;
+                if (!wait1(&bars[kVFull + vs], (w.u / L::VST) & 1)) return false;
+                tc::fence_after_sync();
+                const uint32_t vb = base + L::V + vs * L::TILE;
+                const uint32_t tp = tmem + hh * 128, to = tmem + 256 + hh * 128;
+                const int steps = w.nodes ? kTreeMaxNodes / 16 : BN / 16;
+                for (int kk = 0; kk < steps; ++kk)
+                    tc::mma_bf16_ts(to, tp + kk * 8, tc::smem_desc_sw128(vb + kk * 2048, kBlk, 1024), idPV,
+                                    (!w.first || kk > 0) ? 1u : 0u);
+                tc::mma_commit(&bars[kODone + hh]);
+                if (!PAIR || hh == 1) tc::mma_commit(&bars[kVEmpty + vs]);
+                w.u = -1;
+                return true;
+            };
+            auto issue_s = [&](int hh, uint32_t kbase) {
+                const uint32_t qb = base + L::Q + (PAIR ? hh : 0) * L::TILE;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = (kk >> 2) * kBlk + (kk & 3) * 32;
+                    tc::mma_bf16_ss(tmem + hh * 128, tc::smem_desc_sw128(qb + off, 16, 1024),
+                                    tc::smem_desc_sw128(kbase + off, 16, 1024), idS, kk > 0 ? 1u : 0u);
+                }
+                tc::mma_commit(&bars[kSFull + hh]);
+            };
+            bool ok = true;
+            int u = 0, seg = 0, g[2] = {0, 0}, k[2] = {0, 0};
+            for (; ok && it.next(p, sg); ++seg) {
+                for (int t = sg.t0; t < sg.t1; ++t, ++u) {
+                    const int i = t - sg.t0, st = u % L::KST;
+                    if (!wait1(&bars[kKFull + st], (u / L::KST) & 1) || *abort_flag) { ok = false; break; }
+                    const uint32_t kbase = base + L::K + st * L::TILE;
+                    const bool last = t == sg.t1 - 1;
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {
+                        if (!PAIR && hh != (i & 1)) continue;
+                        if (owed[hh].u >= 0 && !issue_pv(hh)) { ok = false; break; }
+                        if (i == 0 && !wait1(&bars[kQFull + hh], seg & 1)) { ok = false; break; }
+                        tc::fence_after_sync();
+                        issue_s(hh, kbase);
+                        if (last) tc::mma_commit(&bars[kQEmpty + (PAIR ? hh : 0)]);
+                        if (!PAIR || hh == 1) tc::mma_commit(&bars[kKEmpty + st]);
+                        owed[hh] = {u, g[hh]++, seg, k[hh], i == (PAIR ? 0 : hh), t == sg.n_ctx_tiles};
+                    }
+                    if (!ok) break;
+                }
+                if (!ok) break;
+                ++k[0];
+                if (PAIR || sg.t1 - sg.t0 >= 2) ++k[1];
+                // a one-tile segment leaves chain B out: what an older segment owes
+                // it cannot wait for its next tile, since chain A waits for it
+                if (!PAIR && owed[1].u >= 0 && owed[1].seg < seg) ok = issue_pv(1);
+            }
+            if (ok && !*abort_flag) {
+                const int a = owed[1].u >= 0 && (owed[0].u < 0 || owed[1].u < owed[0].u) ? 1 : 0;
+                if (owed[a].u >= 0) ok = issue_pv(a);
+                if (ok && owed[a ^ 1].u >= 0) ok = issue_pv(a ^ 1);
+            }
+            if (!ok) *abort_flag = 1;
+            // every MMA issued by this thread has finished before TMEM is freed
+            tc::mma_commit(&bars[kDrain]);
+            wait1(&bars[kDrain], 0);
+        }
+    } else {
+        // ------------------------------------------------------------ softmax
+        const int hh = warp >> 2;
+        const int r = threadIdx.x & 127;           // row in tile == TMEM lane
+        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + hh * 128 + lane_off;
+        const uint32_t tO = tmem + 256 + hh * 128 + lane_off;
+        const uint64_t sl2 = tc::f2_pack(p.scale_log2, p.scale_log2);
+        float2 *s_ml = reinterpret_cast<float2 *>(sbase + L::ML);
+        bool ok = true;
+        int u = 0, seg = 0, g[2] = {0, 0}, k[2] = {0, 0};   // as the issuer's
+        for (; ok && it.next(p, sg); ++seg) {
+            const int nt = sg.t1 - sg.t0;
+            const int row = sg.rt * RS + (PAIR ? hh * 128 : 0) + r;   // of the stream's KV head
+            const int node = row / G;
+            const bool live = node < sg.n;
+            const bool active = __any_sync(0xffffffffu, live);        // some row of the warp
+            // what this row sees
+            uint64_t vis = 0;
+            RingBounds rb = {-1, -1};
+            RingSpan span;
+            if constexpr (RING) {
+                const int64_t *np = p.node_pos + (int64_t)sg.b * p.N;
+                const int64_t p0 = lane < sg.n ? np[lane] : 0, p1 = lane + 32 < sg.n ? np[lane + 32] : 0;
+                int lo0 = INT32_MAX, lo1 = -1, hi0 = INT32_MAX, hi1 = -1;
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (lane + 32 * e < sg.n) {
+                        const RingBounds x = ring_bounds(e ? p1 : p0, p.window);
+                        lo0 = min(lo0, x.lo); lo1 = max(lo1, x.lo);
+                        hi0 = min(hi0, x.hi); hi1 = max(hi1, x.hi);
+                    }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    lo0 = min(lo0, __shfl_xor_sync(0xffffffffu, lo0, o));
+                    lo1 = max(lo1, __shfl_xor_sync(0xffffffffu, lo1, o));
+                    hi0 = min(hi0, __shfl_xor_sync(0xffffffffu, hi0, o));
+                    hi1 = max(hi1, __shfl_xor_sync(0xffffffffu, hi1, o));
+                }
+                span.every = {lo1, hi0};
+                span.any = {lo0, hi1};
+                if (active) {
+                    const int64_t mine = live ? np[node] : 0;
+                    if (live) {
+                        rb = ring_bounds(mine, p.window);
+                        vis = p.mask ? p.mask[(int64_t)sg.b * p.N + node] : (2ull << node) - 1;
+                    }
+                    for (int j = 0; j < sg.n; ++j) {
+                        const int64_t other = __shfl_sync(0xffffffffu, j < 32 ? p0 : p1, j & 31);
+                        if ((uint64_t)mine - (uint64_t)other >= (uint64_t)p.window) vis &= ~(1ull << j);
+                    }
+                    if (sg.n < 64) vis &= (1ull << sg.n) - 1;
+                }
+            } else if (live) {
+                vis = visible_nodes<false>(p, sg.b, sg.n, node);
+            }
+
+            float m = -INFINITY, l = 0.f;
+            bool first = true;
+            for (int t = sg.t0; t < sg.t1; ++t, ++u) {
+                if (!PAIR && hh != ((t - sg.t0) & 1)) {
+                    ++g[hh ^ 1];
+                    continue;
+                }
+                const bool nodes = t == sg.n_ctx_tiles;
+                const int64_t j0 = (int64_t)t * BN;
+                // is the tile seen whole by every row?  A ring tile's stored positions
+                // in four registers a lane, slot j0 + lane + 32 e in sp[e]
+                bool masked = nodes || j0 + BN > sg.ctx;
+                int sp[4];
+                if constexpr (RING) {
+                    if (!nodes) {
+                        bool all = true;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int64_t j = j0 + lane + 32 * e;
+                            sp[e] = j < sg.ctx ? p.slot_pos[sg.row0 + j] : -1;
+                            all &= span.every.hi > span.every.lo && span.every.sees(sp[e]);
+                        }
+                        masked = !__all_sync(0xffffffffu, all);
+                    }
+                }
+                if (masked && (!PAIR || hh == 0)) {
+                    // V rows before P V: thread r has key row r
+                    if (!waitw(&bars[kVFull + u % L::VST], (u / L::VST) & 1)) { ok = false; break; }
+                    bool unseen, whole_row = false;
+                    if (nodes) {
+                        unseen = r >= sg.n;
+                    } else if (RING) {
+                        int s = -1;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s = (warp & 3) == e ? sp[e] : s;
+                        unseen = !(span.any.hi > span.any.lo && span.any.sees(s));
+                    } else {
+                        unseen = j0 + r >= sg.ctx;
+                        whole_row = !unseen;   // every row sees it: what it holds counts for all
+                    }
+                    if (!whole_row && !(nodes && r >= kTreeMaxNodes)) {
+                        if (clean_v_row<KB>(sbase + L::V + (u % L::VST) * L::TILE, r, unseen))
+                            *(volatile int *)&misc->poison[seg & 3] = seg;
+                        fence_proxy_async_smem();
+                    }
+                }
+                if (!waitw(&bars[kSFull + hh], g[hh] & 1)) { ok = false; break; }
+                tc::fence_after_sync();
+                if (active) {
+                    float s[BN];
+#pragma unroll
+                    for (int c = 0; c < BN; c += 32) tc::tmem_ld32(tS + c, s + c);
+                    tc::wait_ld();
+                    if (masked) {
+                        uint32_t w[4];
+                        if (nodes) {
+                            w[0] = (uint32_t)vis;
+                            w[1] = (uint32_t)(vis >> 32);
+                            w[2] = w[3] = 0;
+                        } else if constexpr (RING) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                w[e] = 0;
+                                for (int c = 0; c < 32; ++c)
+                                    if (rb.sees(__shfl_sync(0xffffffffu, sp[e], c))) w[e] |= 1u << c;
+                            }
+                        } else {
+                            const int cnt = (int)(sg.ctx - j0);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int x = cnt - 32 * e;
+                                w[e] = x >= 32 ? 0xffffffffu : x <= 0 ? 0u : (1u << x) - 1u;
+                            }
+                        }
+#pragma unroll
+                        for (int c = 0; c < BN; ++c) s[c] = (w[c >> 5] >> (c & 31)) & 1u ? s[c] : -INFINITY;
+                    }
+                    float a8[8];
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk) a8[kk] = tc::max3(s[kk], s[kk + 8], s[kk + 16]);
+#pragma unroll
+                    for (int c = 24; c < 120; c += 16)
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk) a8[kk] = tc::max3(a8[kk], s[c + kk], s[c + 8 + kk]);
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk) a8[kk] = fmaxf(a8[kk], s[120 + kk]);
+                    const float mx = tc::max3(tc::max3(a8[0], a8[1], a8[2]), tc::max3(a8[3], a8[4], a8[5]),
+                                              fmaxf(a8[6], a8[7]));
+                    // the reference moves (and O is rescaled) only when it grows by more than 2^8
+                    const float m_cand = mx * p.scale_log2;
+                    float alpha = 1.f;
+                    const bool grow = m_cand > m + 8.f;
+                    if (grow) {
+                        alpha = m == -INFINITY ? 0.f : tc::ex2(m - m_cand);
+                        m = m_cand;
+                    }
+                    const float neg_m = m == -INFINITY ? 0.f : -m;
+                    const uint64_t nm2 = tc::f2_pack(neg_m, neg_m);
+                    uint64_t rs2a = 0, rs2b = 0;
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t pk[BN / 4];
+#pragma unroll
+                        for (int cc = 0; cc < BN / 2; cc += 2) {
+                            const int c = half * (BN / 2) + cc;
+                            float x0, x1;
+                            tc::f2_unpack(tc::f2_fma(tc::f2_pack(s[c], s[c + 1]), sl2, nm2), x0, x1);
+                            const float e0 = tc::ex2(x0), e1 = tc::ex2(x1);
+                            if (c & 2)
+                                rs2b = tc::f2_add(rs2b, tc::f2_pack(e0, e1));
+                            else
+                                rs2a = tc::f2_add(rs2a, tc::f2_pack(e0, e1));
+                            // P is rounded to bf16 for the tensor core (half a step of each
+                            // weight); the sum takes the weights before that
+                            pk[cc / 2] = tc::pack_bf16x2(e0, e1);
+                        }
+                        tc::tmem_st32u(tS + half * 32, pk);
+                    }
+                    float ra0, ra1, rb0, rb1;
+                    tc::f2_unpack(rs2a, ra0, ra1);
+                    tc::f2_unpack(rs2b, rb0, rb1);
+                    l = l * alpha + ((ra0 + ra1) + (rb0 + rb1));
+                    if (!first && __any_sync(0xffffffffu, grow)) {
+                        if (!waitw(&bars[kODone + hh], (g[hh] - 1) & 1)) { ok = false; break; }
+                        tc::fence_after_sync();
+#pragma unroll
+                        for (int c = 0; c < D; c += 32) {
+                            float o[32];
+                            tc::tmem_ld32(tO + c, o);
+                            tc::wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] *= alpha;
+                            tc::tmem_st32(tO + c, o);
+                        }
+                    }
+                    tc::wait_st();
+                }
+                first = false;
+                tc::fence_before_sync();
+                mbar_arrive(&bars[kPFull + hh]);
+                ++g[hh];
+            }
+            if (!ok) break;
+            const bool has_b = PAIR || nt >= 2;
+            if (!PAIR && hh == 1) {
+                // chain B leaves its statistics for chain A, which joins and writes both
+                if (has_b) {
+                    if (k[1] >= 1 && !waitw(&bars[kOFree + 1], (k[1] - 1) & 1)) { ok = false; break; }
+                    s_ml[r] = make_float2(m, l);
+                    mbar_arrive(&bars[kML]);
+                }
+                ++k[0];
+                k[1] += has_b;
+                continue;
+            }
+            if (!waitw(&bars[kODone + hh], (g[hh] - 1) & 1)) { ok = false; break; }
+            float wa = 1.f, wb = 0.f;
+            const bool join = !PAIR && has_b;
+            if (join) {
+                if (!waitw(&bars[kML], k[1] & 1) || !waitw(&bars[kODone + 1], (g[1] - 1) & 1)) { ok = false; break; }
+                const float2 ml = s_ml[r];
+                const float mm = fmaxf(m, ml.x);
+                const float ref = mm == -INFINITY ? 0.f : mm;
+                wa = tc::ex2(m - ref);
+                wb = tc::ex2(ml.x - ref);
+                l = l * wa + ml.y * wb;
+                m = mm;
+            }
+            tc::fence_after_sync();
+            const bool poison = *(volatile int *)&misc->poison[seg & 3] == seg;
+            const bool none = m == -INFINITY && l == 0.f;   // a NaN sum is not nothing
+            const float inv = none ? 0.f : 1.f / l;
+            const int head = sg.g * G + row % G;
+            const int64_t entry = ((int64_t)blockIdx.x * 2 + sg.slot) * RS + (PAIR ? hh * 128 : 0) + r;
+            __nv_bfloat16 *dst =
+                static_cast<__nv_bfloat16 *>(p.o) + (((int64_t)sg.b * p.N + (live ? node : 0)) * p.Hq + head) * D;
+            if (active) {
+                for (int c = 0; c < D; c += 32) {
+                    float o[32];
+                    tc::tmem_ld32(tO + c, o);
+                    if (join) {
+                        float ob[32];
+                        tc::tmem_ld32(tO + 128 + c, ob);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = o[e] * wa + ob[e] * wb;
+                    } else {
+                        tc::wait_ld();
+                    }
+                    if (poison && live) {
+                        const __nv_bfloat16 *vn = static_cast<const __nv_bfloat16 *>(p.v_nodes) +
+                                                  ((int64_t)sg.b * p.N * p.Hkv + sg.g) * D + c;
+                        if (sg.t1 > sg.n_ctx_tiles)
+                            for (int j = 0; j < sg.n; ++j)
+                                if ((vis >> j) & 1) add_odd(vn + (int64_t)j * p.Hkv * D, o);
+                        if constexpr (RING) {
+                            const int64_t j1 = sched::min64((int64_t)sg.t1 * BN, sg.ctx);
+                            for (int64_t j = (int64_t)sg.t0 * BN; j < j1; ++j)
+                                if (rb.sees(p.slot_pos[sg.row0 + j]))
+                                    add_odd(static_cast<const __nv_bfloat16 *>(p.v) +
+                                                ((sg.row0 + j) * p.Hkv + sg.g) * D + c, o);
+                        }
+                    }
+                    if (live && sg.whole) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            uint4 wv;
+                            wv.x = tc::pack_bf16x2(o[e] * inv, o[e + 1] * inv);
+                            wv.y = tc::pack_bf16x2(o[e + 2] * inv, o[e + 3] * inv);
+                            wv.z = tc::pack_bf16x2(o[e + 4] * inv, o[e + 5] * inv);
+                            wv.w = tc::pack_bf16x2(o[e + 6] * inv, o[e + 7] * inv);
+                            *reinterpret_cast<uint4 *>(dst + c + e) = wv;
+                        }
+                    } else if (live) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4 *>(p.ws_o + entry * D + c + e) =
+                                make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    }
+                    __syncwarp();   // the TMEM load takes the whole warp
+                }
+            }
+            tc::fence_before_sync();
+            mbar_arrive(&bars[kOFree + hh]);
+            if (join) mbar_arrive(&bars[kOFree + 1]);
+            if (live && sg.whole && p.lse)
+                p.lse[((int64_t)sg.b * p.Hq + head) * p.N + node] = none ? -INFINITY : (m + __log2f(l)) * kLn2;
+            if (live && !sg.whole) p.ws_ml[entry] = make_float2(m, l);
+            ++k[0];
+            k[1] += has_b;
+        }
+        if (!ok) *abort_flag = 1;
+        tc::wait_st();   // no TMEM store may be in flight when TMEM is freed
+    }
+
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 9) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// ------------------------------------------------------------------- host
+namespace {
+
+// 4-D bf16 map over [d3, d2, d1, D] (innermost D), 128-byte swizzle.
+bool make_map(CUtensorMap *m, const void *ptr, int64_t D, int64_t d1, int64_t d2, int64_t d3, int box1, int box2) {
+    const uint64_t dims[4] = {(uint64_t)D, (uint64_t)d1, (uint64_t)d2, (uint64_t)d3};
+    const uint64_t row = (uint64_t)(d1 * D * 2);
+    // an extent of one has no stride of its own
+    const uint64_t strides[3] = {(uint64_t)(D * 2), row, d3 > 1 ? (uint64_t)d2 * row : row};
+    const uint32_t box[4] = {64, (uint32_t)box1, (uint32_t)box2, 1};
+    return encode_bf16_map_4d(m, ptr, dims, strides, box);
+}
+
+template <int D, bool RING, bool PAIR>
+cudaError_t launch_tc(const TreeArgs &a, const TreePlan &pl, cudaStream_t st) {
+    const int G = a.Hq / a.Hkv;
+    CUtensorMap mq, mk, mv, mkn, mvn;
+    const int64_t ctx_rows = RING ? a.window : a.cache_rows, ctx_b = RING ? a.B : 1;
+    if (!make_map(&mq, a.q, D, a.Hq, a.N, a.B, G, 128 / G) || !make_map(&mk, a.k, D, a.Hkv, ctx_rows, ctx_b, 1, BN) ||
+        !make_map(&mv, a.v, D, a.Hkv, ctx_rows, ctx_b, 1, BN) ||
+        !make_map(&mkn, a.k_nodes, D, a.Hkv, a.N, a.B, 1, kTreeMaxNodes) ||
+        !make_map(&mvn, a.v_nodes, D, a.Hkv, a.N, a.B, 1, kTreeMaxNodes))
+        return cudaErrorNotSupported;
+    auto kern = tree_tc_kernel<D, RING, PAIR>;
+    constexpr size_t smem = Smem<D, PAIR>::ALLOC;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    note_launches(1);
+    return launch_pdl(kern, dim3(pl.grid), dim3(kThreads), smem, st, mq, mk, mv, mkn, mvn, make_params(a, pl));
+}
+
+template <int D>
+cudaError_t launch_tc_d(const TreeArgs &a, const TreePlan &pl, cudaStream_t st) {
+    const bool pair = pl.rows == 256;
+    if (a.window > 0) return pair ? launch_tc<D, true, true>(a, pl, st) : launch_tc<D, true, false>(a, pl, st);
+    return pair ? launch_tc<D, false, true>(a, pl, st) : launch_tc<D, false, false>(a, pl, st);
+}
+
+}  // namespace
+}  // namespace tree
+
+cudaError_t launch_tree_tc(const TreeArgs &a, const TreePlan &pl, cudaStream_t st) {
+    if (a.D == 128) return tree::launch_tc_d<128>(a, pl, st);
+    if (a.D == 64) return tree::launch_tc_d<64>(a, pl, st);
+    return cudaErrorNotSupported;
+}
+
+unsigned int read_and_clear_status_tree_tc() {
+    unsigned int h = 0, z = 0;
+    if (cudaMemcpyFromSymbol(&h, g_status_tree_tc, sizeof(h)) != cudaSuccess) return 0;
+    cudaMemcpyToSymbol(g_status_tree_tc, &z, sizeof(z));
+    return h;
+}
+
+}  // namespace yoco
