@@ -418,8 +418,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         masked = !__all_sync(0xffffffffu, all);
                     }
                 }
+                if (!waitw(&bars[kSFull + hh], g[hh] & 1)) { ok = false; break; }
+                tc::fence_after_sync();
                 if (masked && (!PAIR || hh == 0)) {
-                    // V rows before P V: thread r has key row r
+                    // V rows before P V: thread r has key row r.  After S(u), whose
+                    // MMAs were issued after P.V of tile u - VST: that tile's V had
+                    // landed, so the parity below cannot mean an older phase
                     if (!waitw(&bars[kVFull + u % L::VST], (u / L::VST) & 1)) { ok = false; break; }
                     bool unseen, whole_row = false;
                     if (nodes) {
@@ -439,8 +443,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         fence_proxy_async_smem();
                     }
                 }
-                if (!waitw(&bars[kSFull + hh], g[hh] & 1)) { ok = false; break; }
-                tc::fence_after_sync();
                 if (active) {
                     float s[BN];
 #pragma unroll

@@ -81,6 +81,20 @@ def test_cross_tree_long_and_shared_between_ctas(cuda_lib, dtype):
     tr.assert_tree(*run_cross(cuda_lib, q, kn, vn, kc, vc, starts, lens, masks, n_nodes, max_len=8192), ref, dtype)
 
 
+@pytest.mark.parametrize("N,Hq,Hkv,D,lens", [(3, 32, 8, 128, [3255, 6355, 4000, 5121, 3968, 4097, 6000]),
+                                             (2, 16, 2, 128, [20001, 9000, 12345]), (11, 4, 4, 128, [15000, 1, 8191, 130]),
+                                             (30, 16, 2, 128, [4500, 7000])])
+def test_cross_tree_many_tiles_a_segment(cuda_lib, N, Hq, Hkv, D, lens):
+    """Segments of dozens of tiles that start and end anywhere, where V tiles are
+    loaded while others are still in use."""
+    q, kn, vn, kc, vc, starts = cross_case(BF, lens, N, Hq, Hkv, D, 350)
+    rng = np.random.default_rng(N)
+    masks = [tr.random_tree(rng, N)[0] for _ in lens]
+    ref = tr.cross_tree(q, kn, vn, kc, vc, starts, lens, masks)
+    for _ in range(3):
+        tr.assert_tree(*run_cross(cuda_lib, q, kn, vn, kc, vc, starts, lens, masks), ref, BF)
+
+
 @pytest.mark.parametrize("dtype", [BF, FP])
 @pytest.mark.parametrize("N,Hq,Hkv,D", [(6, 4, 2, 64), (64, 8, 2, 128)])
 def test_rows_that_see_nothing(cuda_lib, dtype, N, Hq, Hkv, D):

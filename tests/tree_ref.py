@@ -6,6 +6,8 @@ import math
 import numpy as np
 import torch
 
+from tests.util import BF16_REL_L2, FP32_REL_L2
+
 # Half a step of a rounding to bf16, relative to the value.
 BF16_HALF = torch.finfo(torch.bfloat16).eps / 2
 
@@ -98,7 +100,12 @@ def assert_tree(o, lse, ref, dtype, what=""):
     products of N(0, 1) inputs, scaled by 1 / sqrt(D), are off by at most
     (D + 2) 2^-24 sum|q k| / sqrt(D) < 130 * 2^-24 * 12 < 2^-13, and a weight by
     that relative to itself, in numerator and denominator: 2^-12 in all.  The
-    log-sum takes the scores' 2^-13 and its own roundings, below 2^-12."""
+    log-sum takes the scores' 2^-13 and its own roundings, below 2^-12.
+    Over all outputs together (a flat softmax makes them far smaller than their
+    terms): a rounding is off by 2^-8 / sqrt(3) rms at most, the weights' ones
+    and the output's are independent, so the 2-norm is off by a share of
+    sqrt(2) 2^-8 / sqrt(3) = 3.2e-3 for V of random signs, held to 5e-3; fp32 to
+    the suite's 2e-5."""
     ro, rl, mag = ref
     go, gl = f64(o), f64(lse)
     tol = 2.0 ** -12 * mag + 1e-30
@@ -110,6 +117,8 @@ def assert_tree(o, lse, ref, dtype, what=""):
     bad = ~(np.abs(go - ro) <= tol)
     assert not bad.any(), (f"{what}: {bad.sum()} outputs off, first at {np.argwhere(bad)[0]}: "
                            f"{go[bad][0]} against {ro[bad][0]} (tolerance {tol[bad][0]:.3e})")
+    rel = np.linalg.norm(go - ro) / max(np.linalg.norm(ro), 1e-30)
+    assert rel <= (BF16_REL_L2 if dtype == torch.bfloat16 else FP32_REL_L2), f"{what}: relative 2-norm {rel:.2e}"
     assert np.all(np.abs(gl[~empty] - rl[~empty]) <= 2.0 ** -12), f"{what}: lse off by {np.abs(gl - rl)[~empty].max()}"
 
 
