@@ -186,6 +186,11 @@ YOCO_DEV void tma_prefetch_4d(const CUtensorMap *map, int c0, int c1, int c2, in
                  : "memory");
 }
 
+// Fetch a tensor map (a kernel parameter) before its first copy.
+YOCO_DEV void prefetch_map(const CUtensorMap *map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 YOCO_DEV float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

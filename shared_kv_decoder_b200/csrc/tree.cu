@@ -28,6 +28,7 @@ constexpr int kSimtThreads = 256;
 constexpr int kSimtRows = 32;     // RS of the CUDA-core kernel
 constexpr int kSimtKeys = 64;     // BN of the CUDA-core kernel
 constexpr int kMergeWarps = 8;
+constexpr int kGroupHeads = 8;
 
 template <typename T>
 YOCO_DEV void load16(const T *src, float *f) {
@@ -43,7 +44,7 @@ YOCO_DEV void load16(const T *src, float *f) {
 // in shared memory, and the product leaves such a key out, so what its K and V
 // hold (infinities, NaN) never reaches the row.
 template <typename T, int D, bool RING>
-__global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const Params p) {
+__global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_constant__ Params p) {
     constexpr int RS = kSimtRows, BN = kSimtKeys, PITCH = D + 4, PP = BN + 4;
     constexpr int EPC = Chunk<T>::N, NJ = D / 64;
     extern __shared__ __align__(16) float smem[];
@@ -54,12 +55,9 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const Params p)
     __shared__ RingBounds s_bounds[RS];
     pdl_trigger();
     pdl_wait();
-    if (threadIdx.x < 32) {
-        const Range r = find_range<RING, RS, BN>(p);
-        if (threadIdx.x == 0) s_range = r;
-    }
+    if (threadIdx.x < 32) find_range<RING, RS, BN>(p, &s_range);
     __syncthreads();
-    const int G = p.Hq / p.Hkv;
+    const int G = 1 << p.lg;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     SegIter<RING, RS, BN> it(p, s_range);
     Seg g;
@@ -95,8 +93,8 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const Params p)
 
         for (int t = g.t0; t < g.t1; ++t) {
             const bool nodes = t == g.n_ctx_tiles;
-            const int64_t j0 = nodes ? 0 : (int64_t)t * BN;
-            const int cnt = nodes ? g.n : (int)sched::min64(BN, g.ctx - j0);
+            const int j0 = nodes ? 0 : t * BN;
+            const int cnt = nodes ? g.n : min(BN, g.ctx - j0);
             const int64_t row0 = nodes ? (int64_t)g.b * p.N : g.row0 + j0;
             const T *kb = static_cast<const T *>(nodes ? p.k_nodes : p.k);
             const T *vb = static_cast<const T *>(nodes ? p.v_nodes : p.v);
@@ -226,78 +224,90 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const Params p)
                     p.lse[((int64_t)g.b * p.Hq + h) * p.N + node] =
                         none ? -INFINITY : (m[i] + log2f(L)) * kLn2;
             } else {
-                const int64_t e = ((int64_t)blockIdx.x * 2 + g.slot) * RS + r;
-                if (tx == 0) p.ws_ml[e] = make_float2(m[i], L);
+                const int64_t e = (int64_t)blockIdx.x * 2 + g.slot;
+                if (tx == 0) p.ws_ml[e * RS + r] = make_float2(m[i], L);
 #pragma unroll
                 for (int j = 0; j < NJ; ++j)
-                    *reinterpret_cast<float4 *>(p.ws_o + e * D + 4 * tx + 64 * j) =
+                    p.ws_o[(e * (D / 4) + tx + 16 * j) * RS + r] =
                         make_float4(o[i][4 * j], o[i][4 * j + 1], o[i][4 * j + 2], o[i][4 * j + 3]);
             }
         }
     }
 }
 
-// Joins the partials of shared streams, one warp per (sequence, node, query
-// head); also writes the rows without a node (and every row of a sequence out
-// of range, which it reports): o = 0, lse = -inf.  grid: the CTAs of the
-// kernel before it.
+// Joins the partials of shared streams; also writes the rows without a node
+// (and every row of a sequence out of range, which it reports): o = 0, lse =
+// -inf.  D / 4 lanes have four columns each of one (sequence, node, query
+// head): a warp has one row at D = 128, two at D = 64.  The first partials are
+// loaded before their weights are known.
 template <typename T, int D, bool RING, int RS, int BN>
-__global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const Params p, const int n_cta) {
-    constexpr int DPL = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+__global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const __grid_constant__ Params p) {
+    constexpr int LANES = D / 4, AHEAD = 4;
+    const int sub = threadIdx.x % LANES;
+    const int row = (int)(blockIdx.x * (32 * kMergeWarps / LANES) + threadIdx.x / LANES);
     pdl_trigger();
     pdl_wait();
-    if (row >= (int64_t)p.B * p.N * p.Hq) return;
-    const int h = (int)(row % p.Hq);
-    const int64_t bn = row / p.Hq;
-    const int node = (int)(bn % p.N), b = (int)(bn / p.N);
-    const int G = p.Hq / p.Hkv;
+    if (row >= p.B * p.N * p.Hq) return;
+    const int bn = row / p.Hq, h = row - bn * p.Hq;
+    const int b = bn / p.N, node = bn - b * p.N;
+    const int T_all = p.prefix[p.B], base = p.prefix[b];
     const Seq s = sequence<RING, RS, BN>(p, b);
-    T *dst = static_cast<T *>(p.o) + row * D + lane * DPL;
-    float *lse = p.lse ? p.lse + ((int64_t)b * p.Hq + h) * p.N + node : nullptr;
-    float M = -INFINITY, L = 0.f, acc[DPL];
-#pragma unroll
-    for (int e = 0; e < DPL; ++e) acc[e] = 0.f;
+    float M = -INFINITY, L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (node < s.n) {
-        const int rr = node * G + h % G;
-        const int64_t T_all = p.prefix[p.B], grid = sched::min64(T_all, n_cta);
+        const int g = h >> p.lg, rr = (node << p.lg) + (h & ((1 << p.lg) - 1));
+        const Deal d(T_all, min(T_all, p.groups));
         const int nt = s.n_ctx_tiles + 1;
-        const int64_t a = p.prefix[b] + (int64_t)((rr / RS) * p.Hkv + h / G) * nt;
-        const int64_t c0 = range_owner(T_all, a, grid), c1 = range_owner(T_all, a + nt - 1, grid);
+        const int a = base + (rr / RS * (p.Hkv / p.heads) + g / p.heads) * nt;
+        const int c0 = d.owner(a), c1 = d.owner(a + nt - 1);
         if (c0 == c1) return;   // finished by its CTA
-        // the stream's part in c0 opens c0's range only when it starts there
-        const int64_t first = c0 * 2 + (range_start(T_all, c0, grid) == a ? 0 : 1);
-        const int n_part = (int)(c1 - c0) + 1;
-        auto entry = [&](int i) { return (i == 0 ? first : (c0 + i) * 2) * RS + rr % RS; };
-        for (int i = lane; i < n_part; i += 32) M = fmaxf(M, p.ws_ml[entry(i)].x);
-        M = warp_max(M);
-        const float ref = M == -INFINITY ? 0.f : M;
-        for (int i0 = 0; i0 < n_part; i0 += 32) {
-            float w = 0.f;
-            if (i0 + lane < n_part) {
-                const float2 ml = p.ws_ml[entry(i0 + lane)];
-                w = exp2f(ml.x - ref);
-                L += ml.y * w;
-            }
-            const int cnt = min(32, n_part - i0);
-#pragma unroll 4
-            for (int i = 0; i < cnt; ++i) {
-                const float wi = __shfl_sync(0xffffffffu, w, i);
-                const float *src = p.ws_o + entry(i0 + i) * D + lane * DPL;
+        const int n_part = c1 - c0 + 1;
+        // the stream's part in c0 opens c0's share only when it starts there
+        const int first = d.start(c0) == a ? 0 : 1;
+        auto entry = [&](int i) { return (int64_t)((c0 + i) * p.heads + g % p.heads) * 2 + (i == 0 ? first : 0); };
+        const int r = rr % RS;
+        for (int i0 = 0; i0 < n_part; i0 += AHEAD) {
+            float2 ml[AHEAD];
+            float4 o[AHEAD];
 #pragma unroll
-                for (int e = 0; e < DPL; ++e) acc[e] = fmaf(wi, src[e], acc[e]);
+            for (int u = 0; u < AHEAD; ++u) {
+                ml[u] = make_float2(-INFINITY, 0.f);
+                o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i0 + u < n_part) {
+                    const int64_t e = entry(i0 + u);
+                    ml[u] = p.ws_ml[e * RS + r];
+                    o[u] = p.ws_o[(e * LANES + sub) * RS + r];
+                }
             }
+            float mx = M;
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) mx = fmaxf(mx, ml[u].x);
+            const float ref = mx == -INFINITY ? 0.f : mx;
+            const float keep = exp2f(M - ref);
+            L *= keep;
+            acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) {
+                const float w = exp2f(ml[u].x - ref);
+                L = fmaf(w, ml[u].y, L);
+                acc.x = fmaf(w, o[u].x, acc.x);
+                acc.y = fmaf(w, o[u].y, acc.y);
+                acc.z = fmaf(w, o[u].z, acc.z);
+                acc.w = fmaf(w, o[u].w, acc.w);
+            }
+            M = mx;
         }
-        L = warp_sum(L);
-    } else if (!s.ok && node == 0 && h == 0 && lane == 0) {
+    } else if (!s.ok && node == 0 && h == 0 && sub == 0) {
         atomicOr(&g_status_tree, kStatusBadSequence);
     }
     const bool none = M == -INFINITY && L == 0.f;
     const float inv = none ? 0.f : 1.f / L;
+    T *dst = static_cast<T *>(p.o) + (int64_t)row * D + 4 * sub;
+    const float v[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
 #pragma unroll
-    for (int e = 0; e < DPL; ++e) dst[e] = from_f32<T>(acc[e] * inv);
-    if (lse && lane == 0) *lse = none ? -INFINITY : (M + log2f(L)) * kLn2;
+    for (int e = 0; e < 4; ++e) dst[e] = from_f32<T>(v[e]);
+    if (p.lse && sub == 0)
+        p.lse[((int64_t)b * p.Hq + h) * p.N + node] = none ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
 // ------------------------------------------------------------------- host
@@ -310,15 +320,16 @@ cudaError_t launch_simt(const TreeArgs &a, const TreePlan &pl, cudaStream_t st) 
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     note_launches(1);
-    return launch_pdl(kern, dim3(pl.grid), dim3(kSimtThreads), smem, st, make_params(a, pl));
+    return launch_pdl(kern, dim3(pl.heads * pl.groups), dim3(kSimtThreads), smem, st, make_params(a, pl));
 }
 
 template <typename T, int D, bool RING, int RS, int BN>
 cudaError_t launch_merge(const TreeArgs &a, const TreePlan &pl, cudaStream_t st) {
+    constexpr int per_cta = 32 * kMergeWarps / (D / 4);
     const int64_t rows = (int64_t)a.B * a.N * a.Hq;
     note_launches(1);
-    return launch_pdl(tree_merge_kernel<T, D, RING, RS, BN>, dim3((unsigned)((rows + kMergeWarps - 1) / kMergeWarps)),
-                      dim3(32 * kMergeWarps), 0, st, make_params(a, pl), pl.grid);
+    return launch_pdl(tree_merge_kernel<T, D, RING, RS, BN>, dim3((unsigned)((rows + per_cta - 1) / per_cta)),
+                      dim3(32 * kMergeWarps), 0, st, make_params(a, pl));
 }
 
 template <int D, bool RING>
@@ -342,14 +353,18 @@ bool make_tree_plan(int32_t B, int32_t N, int64_t max_len, int Hq, int Hkv, int 
     // bf16: the tensor-core kernel, one row tile of 128 or two; fp32: CUDA cores
     pl.rows = dtype != kBF16 ? tree::kSimtRows : N * (Hq / Hkv) <= 128 ? 128 : 256;
     pl.keys = dtype != kBF16 ? tree::kSimtKeys : tree::kTcKeys;
-    // streams and tiles at full length: no CTA without a tile is launched
-    const int64_t streams = (int64_t)B * ((N * (Hq / Hkv) + pl.rows - 1) / pl.rows) * Hkv;
-    const int64_t tiles = streams * ((max_len + pl.keys - 1) / pl.keys + 1);
-    if ((int64_t)B * N * Hq > (int64_t)INT32_MAX || tiles > (INT64_MAX >> 16)) return false;
-    const int per_sm = dtype != kBF16 ? 2 : 1;
-    pl.grid = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, (int64_t)per_sm * device_sm_count()));
-    pl.ml_off = ((size_t)(B + 1) * sizeof(int64_t) + 15) / 16 * 16;
-    const size_t entries = (size_t)pl.grid * 2 * pl.rows;
+    // groups of CTAs, one KV head of a block each (tree.cuh): the largest divisor of Hkv up to 8
+    pl.heads = 1;
+    for (int h = 2; h <= tree::kGroupHeads; ++h)
+        if (Hkv % h == 0) pl.heads = h;
+    // tiles at full length: no group without a tile is launched
+    const int64_t blocks = (int64_t)B * ((N * (Hq / Hkv) + pl.rows - 1) / pl.rows) * (Hkv / pl.heads);
+    const int64_t tiles = blocks * ((max_len + pl.keys - 1) / pl.keys + 1);
+    if ((int64_t)B * N * Hq > (int64_t)INT32_MAX / 2 || tiles > INT32_MAX / 2) return false;
+    const int64_t ctas = (int64_t)(dtype != kBF16 ? 2 : 1) * device_sm_count();
+    pl.groups = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, ctas / pl.heads));
+    pl.ml_off = ((size_t)(B + 1) * sizeof(int32_t) + 15) / 16 * 16;
+    const size_t entries = (size_t)pl.groups * pl.heads * 2 * pl.rows;
     pl.o_off = pl.ml_off + entries * sizeof(float2);
     pl.ws_bytes = pl.o_off + entries * D * sizeof(float);
     *plan = pl;

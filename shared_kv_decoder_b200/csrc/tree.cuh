@@ -4,17 +4,19 @@
 // Work.  A "stream" is the rows of one (sequence, row block, KV head): RS rows
 // of the row order r = node * G + head-in-group (G = Hq / Hkv), against that
 // sequence's keys in tiles of BN -- first the context (the cache's rows, or the
-// ring's slots), then one tile with the drafted nodes' own keys.  All streams'
-// tiles are numbered sequence by sequence (row block outermost, then KV head,
-// then tile), and CTA c of G takes the range [c T / G, (c + 1) T / G) of the T
-// tiles (G no more than T, so that none is empty): every CTA gets the same
-// number to within one whatever the lengths are, and a long stream is shared by as many CTAs as it has work for.  Row
-// blocks of one sequence follow one another, so the CTAs that read the same
-// keys for different rows do it at about the same time (from L2).  A CTA's
-// part of a stream is a segment.  A stream that one CTA has whole is finished
-// by it; of one that is shared, each CTA leaves a partial (m, l, unnormalised
-// o) in the workspace, slot 0 for the segment its range opens with, slot 1 for
-// the one it ends with, and tree_merge_kernel joins them.
+// ring's slots), then one tile with the drafted nodes' own keys.  The CTAs come
+// in groups of `heads`, one KV head each, which walk the same tiles side by
+// side: a token's K (or V) of all heads is one run in memory (8 heads of 128:
+// 64 nodes over 131007 tokens 189 us, 197 us in groups of one; 16 sequences of
+// 64K-128K tokens 1034 and 1028 us).
+// The tiles of (sequence, row block, head block) are numbered sequence by
+// sequence, and group c of C takes a contiguous share of the T tiles, T / C of
+// them to within one: every CTA gets the same work whatever the lengths are,
+// and a long stream is shared by as many CTAs as it has work for.  A CTA's part
+// of a stream is a segment.  A stream that one CTA has whole is finished by it;
+// of one that is shared, each CTA leaves a partial (m, l, unnormalised o) in
+// the workspace, slot 0 for the segment its share opens with, slot 1 for the
+// one it ends with, and tree_merge_kernel joins them.
 #pragma once
 
 #include "common.cuh"
@@ -36,29 +38,31 @@ struct Params {
     const uint64_t *mask;                // [B, N] or null (a chain)
     const int32_t *n_nodes;              // [B] or null (N each)
     int32_t B, N, Hq, Hkv;
+    int32_t lg;                          // log2 of Hq / Hkv
+    int32_t heads, groups;               // KV heads of a CTA group; groups
     int32_t window;                      // 0: cache
     int64_t cache_rows, max_len;
     float scale_log2;
     void *o;                             // [B, N, Hq, D]
     float *lse;                          // [B, Hq, N] or null
-    int64_t *prefix;                     // workspace: first tile of each sequence, then the total
+    int32_t *prefix;                     // workspace: first tile of each sequence, then the total
     float2 *ws_ml;                       // workspace: [2 grid][RS]
-    float *ws_o;                         // workspace: [2 grid][RS][D]
+    float4 *ws_o;                        // workspace: [2 grid][D / 4][RS], a row's four columns each
 };
 
 // One sequence: its nodes (0 when it has none or is out of range), context
-// keys, context tiles and streams.
+// keys, context tiles and row blocks.
 struct Seq {
     int n, n_ctx_tiles, n_rt;
-    int64_t ctx, row0;
+    int ctx;
+    int64_t row0;
     bool ok;
-    YOCO_DEV int64_t tiles(int Hkv) const { return (int64_t)n_rt * Hkv * (n_ctx_tiles + 1); }
+    YOCO_DEV int tiles(const Params &p) const { return n_rt * (p.Hkv / p.heads) * (n_ctx_tiles + 1); }
 };
 
 template <bool RING, int RS, int BN>
 YOCO_DEV Seq sequence(const Params &p, int b) {
     Seq s;
-    const int G = p.Hq / p.Hkv;
     const int n = p.n_nodes ? p.n_nodes[b] : p.N;
     s.ok = n >= 0 && n <= p.N;
     if (RING) {
@@ -72,61 +76,75 @@ YOCO_DEV Seq sequence(const Params &p, int b) {
                                    : sched::decode_seq_ok(s.row0, s.ctx, p.max_len, p.cache_rows));
     }
     s.n = s.ok ? n : 0;
-    s.n_ctx_tiles = s.ok ? (int)((s.ctx + BN - 1) / BN) : 0;
-    s.n_rt = (s.n * G + RS - 1) / RS;
+    s.n_ctx_tiles = s.ok ? (int)(((unsigned)s.ctx + BN - 1) / BN) : 0;
+    s.n_rt = (int)(((unsigned)(s.n << p.lg) + RS - 1) / RS);
     return s;
 }
 
-YOCO_DEV int64_t range_start(int64_t T, int64_t c, int64_t grid) { return c * T / grid; }
-YOCO_DEV int64_t range_owner(int64_t T, int64_t x, int64_t grid) { return ((x + 1) * grid - 1) / T; }
+// Shares of T tiles for C groups, C <= T: the first T mod C get one more.
+struct Deal {
+    int q, rem;
+    YOCO_DEV Deal(int T, int C) : q(T / C), rem(T - q * C) {}
+    YOCO_DEV int start(int c) const { return c * q + min(c, rem); }
+    YOCO_DEV int owner(int x) const {
+        const int cut = rem * (q + 1);
+        return x < cut ? x / (q + 1) : rem + (x - cut) / q;
+    }
+};
 
-// Where a CTA's range starts: the range [x, end), the sequence that holds x and
-// that sequence's first tile.  Run by one whole warp; CTA 0 also leaves the
-// prefix of tile counts in the workspace for the merge.
+// Where a CTA's share starts: tiles [x, end), the sequence that holds x and
+// that sequence's first tile.  Run by one whole warp into shared memory; CTA 0
+// also leaves the prefix of tile counts in the workspace for the merge.
 struct Range {
-    int64_t x, end, base;
-    int b;
+    int x, end, base, b;
+    Seq s;
 };
 
 template <bool RING, int RS, int BN>
-YOCO_DEV Range find_range(const Params &p) {
+YOCO_DEV void find_range(const Params &p, Range *out) {
     const int lane = threadIdx.x & 31;
-    int64_t T = 0;
-    for (int b = lane; b < p.B; b += 32) T += sequence<RING, RS, BN>(p, b).tiles(p.Hkv);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) T += __shfl_xor_sync(0xffffffffu, T, o);
-    Range r;
-    const int64_t grid = sched::min64(T, gridDim.x);
-    r.x = r.end = T;
-    if (blockIdx.x < grid) {
-        r.x = range_start(T, blockIdx.x, grid);
-        r.end = range_start(T, blockIdx.x + 1, grid);
+    const Seq none = {};
+    const Seq s0 = lane < p.B ? sequence<RING, RS, BN>(p, lane) : none;
+    const int t0 = s0.tiles(p);
+    int T = t0;
+    for (int b = lane + 32; b < p.B; b += 32) T += sequence<RING, RS, BN>(p, b).tiles(p);
+    T = __reduce_add_sync(0xffffffffu, T);
+    const int C = min(T, p.groups), c = (int)blockIdx.x / p.heads;
+    int x = T, end = T;
+    if (c < C) {
+        const Deal d(T, C);
+        x = d.start(c);
+        end = d.start(c + 1);
     }
-    r.b = p.B;
-    r.base = T;
-    bool found = r.x >= r.end;
-    int64_t base = 0;
+    bool found = x >= end;
+    if (lane == 0) {
+        out->x = x;
+        out->end = end;
+    }
+    int base = 0;
     for (int b0 = 0; b0 < p.B && (!found || blockIdx.x == 0); b0 += 32) {
         const int b = b0 + lane;
-        const int64_t cnt = b < p.B ? sequence<RING, RS, BN>(p, b).tiles(p.Hkv) : 0;
-        int64_t incl = cnt;
+        const Seq s = b0 == 0 ? s0 : b < p.B ? sequence<RING, RS, BN>(p, b) : none;
+        const int cnt = b0 == 0 ? t0 : s.tiles(p);
+        int incl = cnt;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += y;
         }
-        const unsigned hit = __ballot_sync(0xffffffffu, base + incl > r.x);
+        const unsigned hit = __ballot_sync(0xffffffffu, base + incl > x);
         if (!found && hit) {
-            const int src = __ffs(hit) - 1;
-            r.b = b0 + src;
-            r.base = __shfl_sync(0xffffffffu, base + incl - cnt, src);
+            if (lane == __ffs(hit) - 1) {
+                out->b = b;
+                out->base = base + incl - cnt;
+                out->s = s;
+            }
             found = true;
         }
         if (blockIdx.x == 0 && b < p.B) p.prefix[b] = base + incl - cnt;
         base += __shfl_sync(0xffffffffu, incl, 31);
     }
     if (blockIdx.x == 0 && lane == 0) p.prefix[p.B] = T;
-    return r;
 }
 
 // A segment: tiles [t0, t1) of one stream.
@@ -134,7 +152,8 @@ struct Seg {
     int b, rt, g;        // sequence, row block, KV head
     int n, n_ctx_tiles;  // its nodes and context tiles (tile n_ctx_tiles holds the nodes)
     int t0, t1;
-    int64_t ctx, row0;
+    int ctx;
+    int64_t row0;
     bool whole;          // the CTA has the whole stream
     int slot;            // partial slot otherwise
 };
@@ -143,34 +162,28 @@ struct Seg {
 template <bool RING, int RS, int BN>
 struct SegIter {
     Range r;
-    int64_t x0;
-    Seq s;
-    int64_t tiles;
+    int x0, tiles;
     YOCO_DEV SegIter(const Params &p, const Range &range) : r(range), x0(range.x), tiles(0) {
-        if (r.x < r.end) {
-            s = sequence<RING, RS, BN>(p, r.b);
-            tiles = s.tiles(p.Hkv);
-        }
+        if (r.x < r.end) tiles = r.s.tiles(p);
     }
     YOCO_DEV bool next(const Params &p, Seg &g) {
         if (r.x >= r.end) return false;
         while (r.x >= r.base + tiles) {
             r.base += tiles;
-            s = sequence<RING, RS, BN>(p, ++r.b);
-            tiles = s.tiles(p.Hkv);
+            r.s = sequence<RING, RS, BN>(p, ++r.b);
+            tiles = r.s.tiles(p);
         }
-        const int nt = s.n_ctx_tiles + 1;
-        const int64_t off = r.x - r.base;
-        const int stream = (int)(off / nt);
+        const int nt = r.s.n_ctx_tiles + 1, blocks = p.Hkv / p.heads;
+        const int off = r.x - r.base, stream = off / nt;
         g.b = r.b;
-        g.rt = stream / p.Hkv;
-        g.g = stream - g.rt * p.Hkv;
-        g.n = s.n;
-        g.n_ctx_tiles = s.n_ctx_tiles;
-        g.ctx = s.ctx;
-        g.row0 = s.row0;
-        g.t0 = (int)(off - (int64_t)stream * nt);
-        g.t1 = (int)sched::min64(nt, g.t0 + (r.end - r.x));
+        g.rt = stream / blocks;
+        g.g = (stream - g.rt * blocks) * p.heads + (int)blockIdx.x % p.heads;
+        g.n = r.s.n;
+        g.n_ctx_tiles = r.s.n_ctx_tiles;
+        g.ctx = r.s.ctx;
+        g.row0 = r.s.row0;
+        g.t0 = off - stream * nt;
+        g.t1 = min(nt, g.t0 + (r.end - r.x));
         g.whole = g.t0 == 0 && g.t1 == nt;
         g.slot = r.x == x0 ? 0 : 1;
         r.x += g.t1 - g.t0;
@@ -212,13 +225,15 @@ inline Params make_params(const TreeArgs &a, const TreePlan &pl) {
     p.seq_start = a.seq_start; p.seq_len = a.seq_len; p.slot_pos = a.slot_pos; p.node_pos = a.node_pos;
     p.mask = a.mask; p.n_nodes = a.n_nodes;
     p.B = a.B; p.N = a.N; p.Hq = a.Hq; p.Hkv = a.Hkv; p.window = a.window;
+    p.lg = a.Hq / a.Hkv == 8 ? 3 : a.Hq / a.Hkv == 4 ? 2 : a.Hq / a.Hkv == 2 ? 1 : 0;
+    p.heads = pl.heads; p.groups = pl.groups;
     p.cache_rows = a.cache_rows; p.max_len = a.max_len;
     p.scale_log2 = a.scale * kLog2e;
     p.o = a.o; p.lse = a.lse;
     unsigned char *ws = static_cast<unsigned char *>(a.ws);
-    p.prefix = reinterpret_cast<int64_t *>(ws);
+    p.prefix = reinterpret_cast<int32_t *>(ws);
     p.ws_ml = reinterpret_cast<float2 *>(ws + pl.ml_off);
-    p.ws_o = reinterpret_cast<float *>(ws + pl.o_off);
+    p.ws_o = reinterpret_cast<float4 *>(ws + pl.o_off);
     return p;
 }
 

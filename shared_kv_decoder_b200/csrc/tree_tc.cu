@@ -100,36 +100,40 @@ YOCO_DEV bool waitw(uint64_t *bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, &g_status_tree_tc));
 }
 
-// Does a pair of bf16 hold an infinity or NaN (an exponent of all ones)?
-YOCO_DEV bool odd_pair(uint32_t w) { return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u; }
+// The two bf16 of w that are infinite or NaN (an exponent of all ones), as
+// their sign bits: adding the lowest exponent bit carries into them.
+YOCO_DEV uint32_t odd_bits(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
 YOCO_DEV uint32_t clear_odd(uint32_t w) {
-    if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
-    if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
-    return w;
+    const uint32_t t = odd_bits(w);
+    return w & ~((t >> 15 & 1u) * 0xffffu | (t >> 31) * 0xffff0000u);
 }
 
 // Key row r of a V tile: cleared whole (unseen), or of its infinities and NaN;
-// true when there were any of those.
+// true when there were any of those.  Chunks by the swizzle's order, which
+// keeps a quarter-warp off one bank group.
 template <int KB>
 YOCO_DEV bool clean_v_row(uint8_t *tile, int r, bool unseen) {
-    bool odd = false;
+    uint8_t *row = tile + r * 128;
+    if (unseen) {
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb)
+        for (int c = 0; c < 8 * KB; ++c)
+            *reinterpret_cast<uint4 *>(row + (c >> 3) * kBlk + (((c & 7) ^ (r & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+        return false;
+    }
+    uint32_t odd = 0;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            // by the swizzle's order, which keeps a quarter-warp off one bank group
-            uint4 *at = reinterpret_cast<uint4 *>(tile + kb * kBlk + r * 128 + ((c ^ (r & 7)) << 4));
-            if (unseen) {
-                *at = make_uint4(0, 0, 0, 0);
-                continue;
-            }
+    for (int c = 0; c < 8 * KB; ++c) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(row + (c >> 3) * kBlk + (((c & 7) ^ (r & 7)) << 4));
+        odd |= odd_bits(v.x) | odd_bits(v.y) | odd_bits(v.z) | odd_bits(v.w);
+    }
+    if (odd) {
+        for (int c = 0; c < 8 * KB; ++c) {
+            uint4 *at = reinterpret_cast<uint4 *>(row + (c >> 3) * kBlk + (((c & 7) ^ (r & 7)) << 4));
             const uint4 v = *at;
-            if (odd_pair(v.x) || odd_pair(v.y) || odd_pair(v.z) || odd_pair(v.w)) {
-                odd = true;
-                *at = make_uint4(clear_odd(v.x), clear_odd(v.y), clear_odd(v.z), clear_odd(v.w));
-            }
+            *at = make_uint4(clear_odd(v.x), clear_odd(v.y), clear_odd(v.z), clear_odd(v.w));
         }
-    return odd;
+    }
+    return odd != 0;
 }
 
 // The infinities and NaN of one seen V row, added to 32 columns of its output.
@@ -169,9 +173,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     Misc *misc = reinterpret_cast<Misc *>(sbase + L::MISC);
     volatile int *abort_flag = &misc->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int G = p.Hq / p.Hkv;
 
     pdl_trigger();
+    if (threadIdx.x == 32) {
+        tc::prefetch_map(&tm_q);
+        tc::prefetch_map(&tm_k);
+        tc::prefetch_map(&tm_v);
+        tc::prefetch_map(&tm_kn);
+        tc::prefetch_map(&tm_vn);
+    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < 2; ++s) {
             mbar_init(&bars[kQFull + s], 1);
@@ -199,12 +209,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     pdl_wait();
     if (warp == 8) {
-        const Range r = find_range<RING, RS, BN>(p);
-        if (lane == 0) {
-            misc->range = r;
-            // once any CTA has recorded a timeout, the rest of the grid does nothing
-            if (*(volatile unsigned int *)&g_status_tree_tc) misc->range.x = misc->range.end;
-        }
+        find_range<RING, RS, BN>(p, &misc->range);
+        // once any CTA has recorded a timeout, the rest of the grid does nothing
+        if (lane == 0 && *(volatile unsigned int *)&g_status_tree_tc) misc->range.x = misc->range.end;
     }
     tc::fence_before_sync();
     __syncthreads();
@@ -222,9 +229,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int hh = 0; hh < L::QTILES; ++hh) {
                     if (!wait1(&bars[kQEmpty + hh], (k & 1) ^ 1)) { ok = false; break; }
                     mbar_arrive_expect_tx(&bars[kQFull + hh], 128 * D * 2);
-                    const int node0 = (sg.rt * L::QTILES + hh) * (128 / G);
+                    const int node0 = (sg.rt * L::QTILES + hh) * (128 >> p.lg);
                     for (int kb = 0; kb < KB; ++kb)
-                        tc::tma_load_4d(base + L::Q + hh * L::TILE + kb * kBlk, &tm_q, kb * 64, sg.g * G, node0, sg.b,
+                        tc::tma_load_4d(base + L::Q + hh * L::TILE + kb * kBlk, &tm_q, kb * 64, sg.g << p.lg, node0, sg.b,
                                         &bars[kQFull + hh]);
                 }
                 if (!ok) { *abort_flag = 1; ++k; break; }
@@ -350,48 +357,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (; ok && it.next(p, sg); ++seg) {
             const int nt = sg.t1 - sg.t0;
             const int row = sg.rt * RS + (PAIR ? hh * 128 : 0) + r;   // of the stream's KV head
-            const int node = row / G;
+            const int node = row >> p.lg;
             const bool live = node < sg.n;
             const bool active = __any_sync(0xffffffffu, live);        // some row of the warp
-            // what this row sees
+            // what this row sees; the nodes only matter to the segment with their tile
+            const bool with_nodes = sg.t1 > sg.n_ctx_tiles;
             uint64_t vis = 0;
+            if (with_nodes && live) vis = p.mask ? p.mask[(int64_t)sg.b * p.N + node] : (2ull << node) - 1;
             RingBounds rb = {-1, -1};
             RingSpan span;
             if constexpr (RING) {
+                // lane j has nodes j and j + 32
                 const int64_t *np = p.node_pos + (int64_t)sg.b * p.N;
                 const int64_t p0 = lane < sg.n ? np[lane] : 0, p1 = lane + 32 < sg.n ? np[lane + 32] : 0;
-                int lo0 = INT32_MAX, lo1 = -1, hi0 = INT32_MAX, hi1 = -1;
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    if (lane + 32 * e < sg.n) {
-                        const RingBounds x = ring_bounds(e ? p1 : p0, p.window);
-                        lo0 = min(lo0, x.lo); lo1 = max(lo1, x.lo);
-                        hi0 = min(hi0, x.hi); hi1 = max(hi1, x.hi);
-                    }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) {
-                    lo0 = min(lo0, __shfl_xor_sync(0xffffffffu, lo0, o));
-                    lo1 = max(lo1, __shfl_xor_sync(0xffffffffu, lo1, o));
-                    hi0 = min(hi0, __shfl_xor_sync(0xffffffffu, hi0, o));
-                    hi1 = max(hi1, __shfl_xor_sync(0xffffffffu, hi1, o));
-                }
-                span.every = {lo1, hi0};
-                span.any = {lo0, hi1};
+                RingBounds x0 = ring_bounds(p0, p.window), x1 = ring_bounds(p1, p.window);
+                const bool e0 = lane < sg.n, e1 = lane + 32 < sg.n;
+                span.any.lo = __reduce_min_sync(0xffffffffu, min(e0 ? x0.lo : INT32_MAX, e1 ? x1.lo : INT32_MAX));
+                span.every.lo = __reduce_max_sync(0xffffffffu, max(e0 ? x0.lo : -1, e1 ? x1.lo : -1));
+                span.every.hi = __reduce_min_sync(0xffffffffu, min(e0 ? x0.hi : INT32_MAX, e1 ? x1.hi : INT32_MAX));
+                span.any.hi = __reduce_max_sync(0xffffffffu, max(e0 ? x0.hi : -1, e1 ? x1.hi : -1));
                 if (active) {
-                    const int64_t mine = live ? np[node] : 0;
-                    if (live) {
-                        rb = ring_bounds(mine, p.window);
-                        vis = p.mask ? p.mask[(int64_t)sg.b * p.N + node] : (2ull << node) - 1;
+                    const int src = node & 31;
+                    const int lo0 = __shfl_sync(0xffffffffu, x0.lo, src), hi0 = __shfl_sync(0xffffffffu, x0.hi, src);
+                    const int lo1 = __shfl_sync(0xffffffffu, x1.lo, src), hi1 = __shfl_sync(0xffffffffu, x1.hi, src);
+                    if (live) rb = node < 32 ? RingBounds{lo0, hi0} : RingBounds{lo1, hi1};
+                    if (with_nodes) {
+                        const int64_t m0 = __shfl_sync(0xffffffffu, p0, src), m1 = __shfl_sync(0xffffffffu, p1, src);
+                        const uint64_t mine = (uint64_t)(node < 32 ? m0 : m1);
+#pragma unroll 4
+                        for (int j = 0; j < sg.n; ++j) {
+                            const int64_t other = __shfl_sync(0xffffffffu, j < 32 ? p0 : p1, j & 31);
+                            if (mine - (uint64_t)other >= (uint64_t)p.window) vis &= ~(1ull << j);
+                        }
                     }
-                    for (int j = 0; j < sg.n; ++j) {
-                        const int64_t other = __shfl_sync(0xffffffffu, j < 32 ? p0 : p1, j & 31);
-                        if ((uint64_t)mine - (uint64_t)other >= (uint64_t)p.window) vis &= ~(1ull << j);
-                    }
-                    if (sg.n < 64) vis &= (1ull << sg.n) - 1;
                 }
-            } else if (live) {
-                vis = visible_nodes<false>(p, sg.b, sg.n, node);
             }
+            if (sg.n < 64) vis &= (1ull << sg.n) - 1;
 
             float m = -INFINITY, l = 0.f;
             bool first = true;
@@ -401,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     continue;
                 }
                 const bool nodes = t == sg.n_ctx_tiles;
-                const int64_t j0 = (int64_t)t * BN;
+                const int j0 = t * BN;
                 // is the tile seen whole by every row?  A ring tile's stored positions
                 // in four registers a lane, slot j0 + lane + 32 e in sp[e]
                 bool masked = nodes || j0 + BN > sg.ctx;
@@ -411,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         bool all = true;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int64_t j = j0 + lane + 32 * e;
+                            const int j = j0 + lane + 32 * e;
                             sp[e] = j < sg.ctx ? p.slot_pos[sg.row0 + j] : -1;
                             all &= span.every.hi > span.every.lo && span.every.sees(sp[e]);
                         }
@@ -455,14 +456,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                             w[1] = (uint32_t)(vis >> 32);
                             w[2] = w[3] = 0;
                         } else if constexpr (RING) {
+                            // node by node of the warp's rows: a ballot is the node's word
+#pragma unroll 4
+                            for (int i = 0; i < 32 >> p.lg; ++i) {
+                                const RingBounds x = {__shfl_sync(0xffffffffu, rb.lo, i << p.lg),
+                                                      __shfl_sync(0xffffffffu, rb.hi, i << p.lg)};
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                w[e] = 0;
-                                for (int c = 0; c < 32; ++c)
-                                    if (rb.sees(__shfl_sync(0xffffffffu, sp[e], c))) w[e] |= 1u << c;
+                                for (int e = 0; e < 4; ++e) {
+                                    const uint32_t word = __ballot_sync(0xffffffffu, x.sees(sp[e]));
+                                    if (lane >> p.lg == i) w[e] = word;
+                                }
                             }
                         } else {
-                            const int cnt = (int)(sg.ctx - j0);
+                            const int cnt = sg.ctx - j0;
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 const int x = cnt - 32 * e;
@@ -567,8 +573,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool poison = *(volatile int *)&misc->poison[seg & 3] == seg;
             const bool none = m == -INFINITY && l == 0.f;   // a NaN sum is not nothing
             const float inv = none ? 0.f : 1.f / l;
-            const int head = sg.g * G + row % G;
-            const int64_t entry = ((int64_t)blockIdx.x * 2 + sg.slot) * RS + (PAIR ? hh * 128 : 0) + r;
+            const int head = (sg.g << p.lg) + (row & ((1 << p.lg) - 1));
+            const int64_t entry = (int64_t)blockIdx.x * 2 + sg.slot;
+            const int ws_row = (PAIR ? hh * 128 : 0) + r;
             __nv_bfloat16 *dst =
                 static_cast<__nv_bfloat16 *>(p.o) + (((int64_t)sg.b * p.N + (live ? node : 0)) * p.Hq + head) * D;
             if (active) {
@@ -591,8 +598,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int j = 0; j < sg.n; ++j)
                                 if ((vis >> j) & 1) add_odd(vn + (int64_t)j * p.Hkv * D, o);
                         if constexpr (RING) {
-                            const int64_t j1 = sched::min64((int64_t)sg.t1 * BN, sg.ctx);
-                            for (int64_t j = (int64_t)sg.t0 * BN; j < j1; ++j)
+                            const int j1 = min(sg.t1 * BN, sg.ctx);
+                            for (int j = sg.t0 * BN; j < j1; ++j)
                                 if (rb.sees(p.slot_pos[sg.row0 + j]))
                                     add_odd(static_cast<const __nv_bfloat16 *>(p.v) +
                                                 ((sg.row0 + j) * p.Hkv + sg.g) * D + c, o);
@@ -611,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     } else if (live) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<float4 *>(p.ws_o + entry * D + c + e) =
+                            p.ws_o[(entry * (D / 4) + (c + e) / 4) * RS + ws_row] =
                                 make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                     }
                     __syncwarp();   // the TMEM load takes the whole warp
@@ -622,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (join) mbar_arrive(&bars[kOFree + 1]);
             if (live && sg.whole && p.lse)
                 p.lse[((int64_t)sg.b * p.Hq + head) * p.N + node] = none ? -INFINITY : (m + __log2f(l)) * kLn2;
-            if (live && !sg.whole) p.ws_ml[entry] = make_float2(m, l);
+            if (live && !sg.whole) p.ws_ml[entry * RS + ws_row] = make_float2(m, l);
             ++k[0];
             k[1] += has_b;
         }
@@ -666,7 +673,7 @@ cudaError_t launch_tc(const TreeArgs &a, const TreePlan &pl, cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     note_launches(1);
-    return launch_pdl(kern, dim3(pl.grid), dim3(kThreads), smem, st, mq, mk, mv, mkn, mvn, make_params(a, pl));
+    return launch_pdl(kern, dim3(pl.heads * pl.groups), dim3(kThreads), smem, st, mq, mk, mv, mkn, mvn, make_params(a, pl));
 }
 
 template <int D>
