@@ -29,6 +29,7 @@ constexpr int kSimtRows = 32;     // RS of the CUDA-core kernel
 constexpr int kSimtKeys = 64;     // BN of the CUDA-core kernel
 constexpr int kMergeWarps = 8;
 constexpr int kGroupHeads = 8;
+constexpr int64_t kFewRows = 4096;   // rows that four merge warps each still serve in about a wave
 
 template <typename T>
 YOCO_DEV void load16(const T *src, float *f) {
@@ -238,43 +239,53 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_co
 // Joins the partials of shared streams; also writes the rows without a node
 // (and every row of a sequence out of range, which it reports): o = 0, lse =
 // -inf.  D / 4 lanes have four columns each of one (sequence, node, query
-// head): a warp has one row at D = 128, two at D = 64.  The first partials are
-// loaded before their weights are known.
-template <typename T, int D, bool RING, int RS, int BN>
+// head).  SPLIT warps share a row's partials: four where there are few rows, so
+// that a long stream's partials are all in flight at once.
+template <typename T, int D, bool RING, int RS, int BN, int SPLIT>
 __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const __grid_constant__ Params p) {
-    constexpr int LANES = D / 4, AHEAD = 4;
-    const int sub = threadIdx.x % LANES;
-    const int row = (int)(blockIdx.x * (32 * kMergeWarps / LANES) + threadIdx.x / LANES);
+    constexpr int LANES = D / 4, AHEAD = 4, ROWS = 32 * kMergeWarps / (LANES * SPLIT);
+    __shared__ float s_ml[SPLIT][ROWS][2];
+    __shared__ float4 s_o[SPLIT][ROWS][SPLIT > 1 ? LANES : 1];
+    const int sub = threadIdx.x % LANES, slot = threadIdx.x / LANES % ROWS, share = threadIdx.x / (LANES * ROWS);
+    const int row = (int)blockIdx.x * ROWS + slot;
+    const bool real = row < p.B * p.N * p.Hq;
+    const int bn = row / p.Hq, h = row - bn * p.Hq;
+    const int b = real ? bn / p.N : 0, node = bn - b * p.N;
     pdl_trigger();
     pdl_wait();
-    if (row >= p.B * p.N * p.Hq) return;
-    const int bn = row / p.Hq, h = row - bn * p.Hq;
-    const int b = bn / p.N, node = bn - b * p.N;
-    const int T_all = p.prefix[p.B], base = p.prefix[b];
+    const int T_all = p.prefix[p.B], part = p.prefix[p.B + 1], base = p.prefix[b];
     const Seq s = sequence<RING, RS, BN>(p, b);
     float M = -INFINITY, L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (node < s.n) {
+    bool write = real;
+    if (real && node < s.n) {
         const int g = h >> p.lg, rr = (node << p.lg) + (h & ((1 << p.lg) - 1));
-        const Deal d(T_all, min(T_all, p.groups));
         const int nt = s.n_ctx_tiles + 1;
-        const int a = base + (rr / RS * (p.Hkv / p.heads) + g / p.heads) * nt;
-        const int c0 = d.owner(a), c1 = d.owner(a + nt - 1);
-        if (c0 == c1) return;   // finished by its CTA
+        const int a = base + (rr / RS * (p.Hkv / p.heads) + g / p.heads) * s.numbered(part);
+        int c0, c1, first = 0;
+        if (part > 0) {
+            c0 = a / part;
+            c1 = (a + nt - 1) / part;
+        } else {
+            const Deal d(T_all, min(T_all, p.groups));
+            c0 = d.owner(a);
+            c1 = d.owner(a + nt - 1);
+            // the stream's part in c0 opens c0's share only when it starts there
+            first = d.start(c0) == a ? 0 : 1;
+        }
         const int n_part = c1 - c0 + 1;
-        // the stream's part in c0 opens c0's share only when it starts there
-        const int first = d.start(c0) == a ? 0 : 1;
+        write = n_part > 1;   // else finished by its CTA
         auto entry = [&](int i) { return (int64_t)((c0 + i) * p.heads + g % p.heads) * 2 + (i == 0 ? first : 0); };
         const int r = rr % RS;
-        for (int i0 = 0; i0 < n_part; i0 += AHEAD) {
+        for (int i0 = share; write && i0 < n_part; i0 += AHEAD * SPLIT) {
             float2 ml[AHEAD];
             float4 o[AHEAD];
 #pragma unroll
             for (int u = 0; u < AHEAD; ++u) {
                 ml[u] = make_float2(-INFINITY, 0.f);
                 o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (i0 + u < n_part) {
-                    const int64_t e = entry(i0 + u);
+                if (i0 + u * SPLIT < n_part) {
+                    const int64_t e = entry(i0 + u * SPLIT);
                     ml[u] = p.ws_ml[e * RS + r];
                     o[u] = p.ws_o[(e * LANES + sub) * RS + r];
                 }
@@ -297,9 +308,34 @@ __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const __gr
             }
             M = mx;
         }
-    } else if (!s.ok && node == 0 && h == 0 && sub == 0) {
+    } else if (real && !s.ok && node == 0 && h == 0 && sub == 0 && share == 0) {
         atomicOr(&g_status_tree, kStatusBadSequence);
     }
+    if constexpr (SPLIT > 1) {
+        if (sub == 0) {
+            s_ml[share][slot][0] = M;
+            s_ml[share][slot][1] = L;
+        }
+        s_o[share][slot][sub] = acc;
+        __syncthreads();
+        if (share != 0) return;
+#pragma unroll
+        for (int w = 1; w < SPLIT; ++w) M = fmaxf(M, s_ml[w][slot][0]);
+        const float ref = M == -INFINITY ? 0.f : M;
+        L = 0.f;
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < SPLIT; ++w) {
+            const float f = exp2f(s_ml[w][slot][0] - ref);
+            const float4 o = s_o[w][slot][sub];
+            L = fmaf(f, s_ml[w][slot][1], L);
+            acc.x = fmaf(f, o.x, acc.x);
+            acc.y = fmaf(f, o.y, acc.y);
+            acc.z = fmaf(f, o.z, acc.z);
+            acc.w = fmaf(f, o.w, acc.w);
+        }
+    }
+    if (!write) return;
     const bool none = M == -INFINITY && L == 0.f;
     const float inv = none ? 0.f : 1.f / L;
     T *dst = static_cast<T *>(p.o) + (int64_t)row * D + 4 * sub;
@@ -325,11 +361,12 @@ cudaError_t launch_simt(const TreeArgs &a, const TreePlan &pl, cudaStream_t st) 
 
 template <typename T, int D, bool RING, int RS, int BN>
 cudaError_t launch_merge(const TreeArgs &a, const TreePlan &pl, cudaStream_t st) {
-    constexpr int per_cta = 32 * kMergeWarps / (D / 4);
     const int64_t rows = (int64_t)a.B * a.N * a.Hq;
+    const bool few = rows <= kFewRows;
+    const int per_cta = 32 * kMergeWarps / (D / 4) / (few ? 4 : 1);
     note_launches(1);
-    return launch_pdl(tree_merge_kernel<T, D, RING, RS, BN>, dim3((unsigned)((rows + per_cta - 1) / per_cta)),
-                      dim3(32 * kMergeWarps), 0, st, make_params(a, pl));
+    return launch_pdl(few ? tree_merge_kernel<T, D, RING, RS, BN, 4> : tree_merge_kernel<T, D, RING, RS, BN, 1>,
+                      dim3((unsigned)((rows + per_cta - 1) / per_cta)), dim3(32 * kMergeWarps), 0, st, make_params(a, pl));
 }
 
 template <int D, bool RING>
@@ -363,7 +400,7 @@ bool make_tree_plan(int32_t B, int32_t N, int64_t max_len, int Hq, int Hkv, int 
     if ((int64_t)B * N * Hq > (int64_t)INT32_MAX / 2 || tiles > INT32_MAX / 2) return false;
     const int64_t ctas = (int64_t)(dtype != kBF16 ? 2 : 1) * device_sm_count();
     pl.groups = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, ctas / pl.heads));
-    pl.ml_off = ((size_t)(B + 1) * sizeof(int32_t) + 15) / 16 * 16;
+    pl.ml_off = ((size_t)(B + 2) * sizeof(int32_t) + 15) / 16 * 16;
     const size_t entries = (size_t)pl.groups * pl.heads * 2 * pl.rows;
     pl.o_off = pl.ml_off + entries * sizeof(float2);
     pl.ws_bytes = pl.o_off + entries * D * sizeof(float);

@@ -12,8 +12,13 @@
 // The tiles of (sequence, row block, head block) are numbered sequence by
 // sequence, and group c of C takes a contiguous share of the T tiles, T / C of
 // them to within one: every CTA gets the same work whatever the lengths are,
-// and a long stream is shared by as many CTAs as it has work for.  A CTA's part
-// of a stream is a segment.  A stream that one CTA has whole is finished by it;
+// and a long stream is shared by as many CTAs as it has work for.  Where a few
+// more tiles a group (kAlignSlack) let every stream be cut into parts of `part`
+// tiles with no group holding pieces of two, it is cut so: a second segment
+// costs a CTA another fill and drain of its pipeline, as long as about five
+// tiles (4 sequences x 16 nodes over the 1024 ring: CTAs of one segment ran 11
+// us, those of two 17).  The streams are then numbered as if they were a
+// multiple of `part` long.  A CTA's part of a stream is a segment.  A stream that one CTA has whole is finished by it;
 // of one that is shared, each CTA leaves a partial (m, l, unnormalised o) in
 // the workspace, slot 0 for the segment its share opens with, slot 1 for the
 // one it ends with, and tree_merge_kernel joins them.
@@ -45,7 +50,7 @@ struct Params {
     float scale_log2;
     void *o;                             // [B, N, Hq, D]
     float *lse;                          // [B, Hq, N] or null
-    int32_t *prefix;                     // workspace: first tile of each sequence, then the total
+    int32_t *prefix;                     // workspace: first tile of each sequence, the total, the part
     float2 *ws_ml;                       // workspace: [2 grid][RS]
     float4 *ws_o;                        // workspace: [2 grid][D / 4][RS], a row's four columns each
 };
@@ -57,7 +62,12 @@ struct Seq {
     int ctx;
     int64_t row0;
     bool ok;
-    YOCO_DEV int tiles(const Params &p) const { return n_rt * (p.Hkv / p.heads) * (n_ctx_tiles + 1); }
+    YOCO_DEV int streams(const Params &p) const { return n_rt * (p.Hkv / p.heads); }
+    // tiles of a stream as numbered
+    YOCO_DEV int numbered(int part) const {
+        const int nt = n_ctx_tiles + 1;
+        return part > 0 ? (nt + part - 1) / part * part : nt;
+    }
 };
 
 template <bool RING, int RS, int BN>
@@ -92,40 +102,57 @@ struct Deal {
     }
 };
 
-// Where a CTA's share starts: tiles [x, end), the sequence that holds x and
-// that sequence's first tile.  Run by one whole warp into shared memory; CTA 0
-// also leaves the prefix of tile counts in the workspace for the merge.
+// Where a CTA's share starts: numbered tiles [x, end), the sequence that holds
+// x and that sequence's first tile.  Run by one whole warp into shared memory;
+// CTA 0 also leaves the numbering in the workspace for the merge.
 struct Range {
-    int x, end, base, b;
+    int x, end, base, b, part;
     Seq s;
 };
+
+constexpr int kAlignSlack = 5;
 
 template <bool RING, int RS, int BN>
 YOCO_DEV void find_range(const Params &p, Range *out) {
     const int lane = threadIdx.x & 31;
     const Seq none = {};
     const Seq s0 = lane < p.B ? sequence<RING, RS, BN>(p, lane) : none;
-    const int t0 = s0.tiles(p);
-    int T = t0;
-    for (int b = lane + 32; b < p.B; b += 32) T += sequence<RING, RS, BN>(p, b).tiles(p);
+    const int m0 = s0.streams(p);
+    int T = m0 * (s0.n_ctx_tiles + 1);
+    for (int b = lane + 32; b < p.B; b += 32) {
+        const Seq s = sequence<RING, RS, BN>(p, b);
+        T += s.streams(p) * (s.n_ctx_tiles + 1);
+    }
     T = __reduce_add_sync(0xffffffffu, T);
     const int C = min(T, p.groups), c = (int)blockIdx.x / p.heads;
-    int x = T, end = T;
-    if (c < C) {
+    int part = 0;
+    if (p.B <= 32 && T > 0 && __reduce_add_sync(0xffffffffu, m0) <= C) {
+        const int least = (T + C - 1) / C;
+        for (int u = least; u <= least + kAlignSlack && part == 0; ++u)
+            if (__reduce_add_sync(0xffffffffu, m0 * ((s0.n_ctx_tiles + u) / u)) <= C) part = u;
+    }
+    int x = 0, end = 0;
+    bool found = T == 0;
+    if (part > 0) {
+        T = part * __reduce_add_sync(0xffffffffu, m0 * ((s0.n_ctx_tiles + part) / part));
+        x = min(c * part, T);
+        end = min(x + part, T);
+    } else if (c < C) {
         const Deal d(T, C);
         x = d.start(c);
         end = d.start(c + 1);
     }
-    bool found = x >= end;
+    found = x >= end;
     if (lane == 0) {
         out->x = x;
         out->end = end;
+        out->part = part;
     }
     int base = 0;
     for (int b0 = 0; b0 < p.B && (!found || blockIdx.x == 0); b0 += 32) {
         const int b = b0 + lane;
         const Seq s = b0 == 0 ? s0 : b < p.B ? sequence<RING, RS, BN>(p, b) : none;
-        const int cnt = b0 == 0 ? t0 : s.tiles(p);
+        const int cnt = s.streams(p) * s.numbered(part);
         int incl = cnt;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -144,7 +171,10 @@ YOCO_DEV void find_range(const Params &p, Range *out) {
         if (blockIdx.x == 0 && b < p.B) p.prefix[b] = base + incl - cnt;
         base += __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (blockIdx.x == 0 && lane == 0) p.prefix[p.B] = T;
+    if (blockIdx.x == 0 && lane == 0) {
+        p.prefix[p.B] = T;
+        p.prefix[p.B + 1] = part;
+    }
 }
 
 // A segment: tiles [t0, t1) of one stream.
@@ -162,19 +192,23 @@ struct Seg {
 template <bool RING, int RS, int BN>
 struct SegIter {
     Range r;
-    int x0, tiles;
-    YOCO_DEV SegIter(const Params &p, const Range &range) : r(range), x0(range.x), tiles(0) {
-        if (r.x < r.end) tiles = r.s.tiles(p);
+    int x0, numbered, tiles;   // of a stream, of the sequence
+    YOCO_DEV SegIter(const Params &p, const Range &range) : r(range), x0(range.x), numbered(0), tiles(0) {
+        if (r.x < r.end) count(p);
+    }
+    YOCO_DEV void count(const Params &p) {
+        numbered = r.s.numbered(r.part);
+        tiles = r.s.streams(p) * numbered;
     }
     YOCO_DEV bool next(const Params &p, Seg &g) {
         if (r.x >= r.end) return false;
         while (r.x >= r.base + tiles) {
             r.base += tiles;
             r.s = sequence<RING, RS, BN>(p, ++r.b);
-            tiles = r.s.tiles(p);
+            count(p);
         }
         const int nt = r.s.n_ctx_tiles + 1, blocks = p.Hkv / p.heads;
-        const int off = r.x - r.base, stream = off / nt;
+        const int off = r.x - r.base, stream = off / numbered;
         g.b = r.b;
         g.rt = stream / blocks;
         g.g = (stream - g.rt * blocks) * p.heads + (int)blockIdx.x % p.heads;
@@ -182,11 +216,12 @@ struct SegIter {
         g.n_ctx_tiles = r.s.n_ctx_tiles;
         g.ctx = r.s.ctx;
         g.row0 = r.s.row0;
-        g.t0 = off - stream * nt;
-        g.t1 = min(nt, g.t0 + (r.end - r.x));
+        g.t0 = off - stream * numbered;
+        const int len = min(numbered - g.t0, r.end - r.x);
+        g.t1 = min(nt, g.t0 + len);
         g.whole = g.t0 == 0 && g.t1 == nt;
         g.slot = r.x == x0 ? 0 : 1;
-        r.x += g.t1 - g.t0;
+        r.x += len;
         return true;
     }
 };

@@ -14,9 +14,10 @@
 // operations; at the measured rates the cache read is the longer one up to about
 // R = 250.
 //
-// Warp roles (320 threads), as in the prefill:
+// Warp roles (384 threads):
 //   warps 0-3, 4-7  softmax chains A and B: thread r owns row r (TMEM lane r)
-//   warp 8          TMA: lane 0 Q, lane 1 K, lane 2 V
+//   warps 8, 10, 11 TMA: K, V, Q (one thread each; a warp of its own for each, so
+//                   that one's wait never holds up another's first copy)
 //   warp 9          MMA issue (one thread)
 // TMEM (512 columns): S_A/P_A, S_B/P_B, O_A, O_B, 128 columns each; P is bf16
 // over the first 64 columns of its S.
@@ -49,7 +50,7 @@ namespace tree {
 namespace {
 
 constexpr int BN = kTcKeys;
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
 constexpr int kTmemCols = 512;
 constexpr uint32_t kBlk = 128 * 128;   // one [128 rows x 128 bytes] swizzled block
 
@@ -220,9 +221,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     Iter it(p, misc->range);
     Seg sg;
 
-    if (warp == 8) {
-        // ------------------------------------------------------ TMA producer
-        if (lane == 0) {
+    if (warp == 8 || warp >= 10) {
+        // ----------------------------------------------------- TMA producers
+        if (lane == 0 && warp == 11) {
             int k = 0;
             for (; !*abort_flag && it.next(p, sg); ++k) {
                 bool ok = true;
@@ -240,8 +241,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (k > 0)
                 for (int hh = 0; hh < L::QTILES; ++hh)
                     if (!wait1(&bars[kQFull + hh], (k - 1) & 1)) break;
-        } else if (lane == 1 || lane == 2) {
-            const bool is_k = lane == 1;
+        } else if (lane == 0) {
+            const bool is_k = warp == 8;
             const int ST = is_k ? L::KST : L::VST;
             uint64_t *full = &bars[is_k ? kKFull : kVFull], *empty = &bars[is_k ? kKEmpty : kVEmpty];
             const CUtensorMap *ctx_map = is_k ? &tm_k : &tm_v, *node_map = is_k ? &tm_kn : &tm_vn;
@@ -269,75 +270,98 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             constexpr uint32_t idS = tc::idesc_bf16(128, BN, false, false);
             constexpr uint32_t idPV = tc::idesc_bf16(128, D, false, true);
-            // the tile whose P.V is still owed to each chain: its tile counters
-            // (the CTA's, the chain's), its segment counters, and whether it
-            // opens its segment / holds the nodes
+            // descriptors as (low, high) words: the low one holds the address and the
+            // leading offset, so a step is one 32-bit addition.  This thread's
+            // instructions between two MMAs are on every chain's critical path.
+            constexpr uint32_t kHi = (1024u >> 4) | 1u << 14 | 2u << 29;
+            constexpr uint32_t kLoS = (16u >> 4) << 16, kLoV = (kBlk >> 4) << 16;
+            const uint32_t q_lo = ((base + L::Q) >> 4) | kLoS;
+            const uint32_t k_lo = ((base + L::K) >> 4) | kLoS;
+            const uint32_t v_lo = ((base + L::V) >> 4) | kLoV;
+            auto desc = [](uint32_t lo) { return (uint64_t)kHi << 32 | lo; };
+            // the tile whose P.V is still owed to a chain
             struct Owed {
-                int u, g, seg, k;
-                bool first, nodes;
-            } owed[2];
-            owed[0].u = owed[1].u = -1;
-            auto issue_pv = [&](int hh) -> bool {
-                Owed &w = owed[hh];
-                const int vs = w.u % L::VST;
-                if (w.first && w.k >= 1 && !wait1(&bars[kOFree + hh], (w.k - 1) & 1)) return false;
-                if (!wait1(&bars[kPFull + hh], w.g & 1)) return false;
-                if (!wait1(&bars[kVFull + vs], (w.u / L::VST) & 1)) return false;
+                uint32_t v_lo, v_parity, p_parity, o_parity;
+                int v_stage, seg;
+                bool any, first, wait_o, nodes;   // first: opens its segment; wait_o: not the chain's first segment
+            } owed_a = {}, owed_b = {};
+            auto issue_pv = [&](int hh, Owed &w) -> bool {
+                if (w.wait_o && !wait1(&bars[kOFree + hh], w.o_parity)) return false;
+                if (!wait1(&bars[kPFull + hh], w.p_parity)) return false;
+                if ((!PAIR || hh == 0) && !wait1(&bars[kVFull + w.v_stage], w.v_parity)) return false;
                 tc::fence_after_sync();
-                const uint32_t vb = base + L::V + vs * L::TILE;
                 const uint32_t tp = tmem + hh * 128, to = tmem + 256 + hh * 128;
-                const int steps = w.nodes ? kTreeMaxNodes / 16 : BN / 16;
-                for (int kk = 0; kk < steps; ++kk)
-                    tc::mma_bf16_ts(to, tp + kk * 8, tc::smem_desc_sw128(vb + kk * 2048, kBlk, 1024), idPV,
-                                    (!w.first || kk > 0) ? 1u : 0u);
+                tc::mma_bf16_ts(to, tp, desc(w.v_lo), idPV, w.first ? 0u : 1u);
+#pragma unroll
+                for (int kk = 1; kk < kTreeMaxNodes / 16; ++kk)
+                    tc::mma_bf16_ts(to, tp + kk * 8, desc(w.v_lo + kk * (2048 >> 4)), idPV, 1u);
+                if (!w.nodes) {
+#pragma unroll
+                    for (int kk = kTreeMaxNodes / 16; kk < BN / 16; ++kk)
+                        tc::mma_bf16_ts(to, tp + kk * 8, desc(w.v_lo + kk * (2048 >> 4)), idPV, 1u);
+                }
                 tc::mma_commit(&bars[kODone + hh]);
-                if (!PAIR || hh == 1) tc::mma_commit(&bars[kVEmpty + vs]);
-                w.u = -1;
+                if (!PAIR || hh == 1) tc::mma_commit(&bars[kVEmpty + w.v_stage]);
+                w.any = false;
                 return true;
             };
-            auto issue_s = [&](int hh, uint32_t kbase) {
-                const uint32_t qb = base + L::Q + (PAIR ? hh : 0) * L::TILE;
+            bool ok = true;
+            int seg = 0, kst = 0, vst = 0;
+            uint32_t k_ph = 0, v_ph = 0;
+            int ga = 0, gb = 0, ka = 0, kb = 0;   // tiles and segments of chain A, B
+            // S of one chain (after the P.V it still owes), then the new debt
+            auto step = [&](int hh, Owed &w, int &g, int k, bool opens, bool last, bool nodes) -> bool {
+                if (w.any && !issue_pv(hh, w)) return false;
+                if (opens && (PAIR || hh == 0) && !wait1(&bars[kQFull + hh], seg & 1)) return false;
+                tc::fence_after_sync();
+                const uint32_t qd = q_lo + (PAIR ? hh * (L::TILE >> 4) : 0), kd = k_lo + kst * (L::TILE >> 4);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = (kk >> 2) * kBlk + (kk & 3) * 32;
-                    tc::mma_bf16_ss(tmem + hh * 128, tc::smem_desc_sw128(qb + off, 16, 1024),
-                                    tc::smem_desc_sw128(kbase + off, 16, 1024), idS, kk > 0 ? 1u : 0u);
+                    const uint32_t off = ((kk >> 2) * kBlk + (kk & 3) * 32) >> 4;
+                    tc::mma_bf16_ss(tmem + hh * 128, desc(qd + off), desc(kd + off), idS, kk > 0 ? 1u : 0u);
                 }
                 tc::mma_commit(&bars[kSFull + hh]);
+                if (last) tc::mma_commit(&bars[kQEmpty + (PAIR ? hh : 0)]);
+                if (!PAIR || hh == 1) tc::mma_commit(&bars[kKEmpty + kst]);
+                w.v_lo = v_lo + vst * (L::TILE >> 4);
+                w.v_stage = vst;
+                w.v_parity = v_ph;
+                w.p_parity = g & 1;
+                w.o_parity = (k - 1) & 1;
+                w.wait_o = opens && k >= 1;
+                w.first = opens;
+                w.nodes = nodes;
+                w.seg = seg;
+                w.any = true;
+                ++g;
+                return true;
             };
-            bool ok = true;
-            int u = 0, seg = 0, g[2] = {0, 0}, k[2] = {0, 0};
             for (; ok && it.next(p, sg); ++seg) {
-                for (int t = sg.t0; t < sg.t1; ++t, ++u) {
-                    const int i = t - sg.t0, st = u % L::KST;
-                    if (!wait1(&bars[kKFull + st], (u / L::KST) & 1) || *abort_flag) { ok = false; break; }
-                    const uint32_t kbase = base + L::K + st * L::TILE;
-                    const bool last = t == sg.t1 - 1;
-#pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
-                        if (!PAIR && hh != (i & 1)) continue;
-                        if (owed[hh].u >= 0 && !issue_pv(hh)) { ok = false; break; }
-                        if (i == 0 && !wait1(&bars[kQFull + hh], seg & 1)) { ok = false; break; }
-                        tc::fence_after_sync();
-                        issue_s(hh, kbase);
-                        if (last) tc::mma_commit(&bars[kQEmpty + (PAIR ? hh : 0)]);
-                        if (!PAIR || hh == 1) tc::mma_commit(&bars[kKEmpty + st]);
-                        owed[hh] = {u, g[hh]++, seg, k[hh], i == (PAIR ? 0 : hh), t == sg.n_ctx_tiles};
-                    }
+                const int nt = sg.t1 - sg.t0, n_ctx = sg.n_ctx_tiles - sg.t0;
+                for (int i = 0; i < nt; ++i) {
+                    if (!wait1(&bars[kKFull + kst], k_ph)) { ok = false; break; }
+                    const bool last = i == nt - 1, nodes = i == n_ctx;
+                    if (PAIR)
+                        ok = step(0, owed_a, ga, ka, i == 0, last, nodes) && step(1, owed_b, gb, kb, i == 0, last, nodes);
+                    else if (i & 1)
+                        ok = step(1, owed_b, gb, kb, i == 1, last, nodes);
+                    else
+                        ok = step(0, owed_a, ga, ka, i == 0, last, nodes);
                     if (!ok) break;
+                    if (++kst == L::KST) { kst = 0; k_ph ^= 1; }
+                    if (++vst == L::VST) { vst = 0; v_ph ^= 1; }
                 }
                 if (!ok) break;
-                ++k[0];
-                if (PAIR || sg.t1 - sg.t0 >= 2) ++k[1];
+                ++ka;
+                if (PAIR || nt >= 2) ++kb;
                 // a one-tile segment leaves chain B out: what an older segment owes
                 // it cannot wait for its next tile, since chain A waits for it
-                if (!PAIR && owed[1].u >= 0 && owed[1].seg < seg) ok = issue_pv(1);
+                if (!PAIR && owed_b.any && owed_b.seg < seg) ok = issue_pv(1, owed_b);
+                if (*abort_flag) ok = false;
             }
-            if (ok && !*abort_flag) {
-                const int a = owed[1].u >= 0 && (owed[0].u < 0 || owed[1].u < owed[0].u) ? 1 : 0;
-                if (owed[a].u >= 0) ok = issue_pv(a);
-                if (ok && owed[a ^ 1].u >= 0) ok = issue_pv(a ^ 1);
-            }
+            // the last debts, in any order: the chains do not wait for each other here
+            if (ok && owed_a.any) ok = issue_pv(0, owed_a);
+            if (ok && owed_b.any) ok = issue_pv(1, owed_b);
             if (!ok) *abort_flag = 1;
             // every MMA issued by this thread has finished before TMEM is freed
             tc::mma_commit(&bars[kDrain]);
@@ -579,6 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __nv_bfloat16 *dst =
                 static_cast<__nv_bfloat16 *>(p.o) + (((int64_t)sg.b * p.N + (live ? node : 0)) * p.Hq + head) * D;
             if (active) {
+#pragma unroll 2
                 for (int c = 0; c < D; c += 32) {
                     float o[32];
                     tc::tmem_ld32(tO + c, o);
