@@ -16,9 +16,16 @@
 //
 // Warp roles (384 threads):
 //   warps 0-3, 4-7  softmax chains A and B: thread r owns row r (TMEM lane r)
-//   warps 8, 10, 11 TMA: K, V, Q (one thread each; a warp of its own for each, so
-//                   that one's wait never holds up another's first copy)
-//   warp 9          MMA issue (one thread)
+//   warps 8, 10     TMA, one thread each (a warp of its own, so that one's wait never
+//                   holds up the other's copies).  PAIR: K, and Q and V.  ALT: Q and
+//                   chain A's K and V, and chain B's: each chain has a ring of its
+//                   own whose stages take K, V, K, V, ... in turn, and waits for
+//                   every one of them, so no parity can mean an older phase
+//   warps 9, 11     MMA issue of chain A and of chain B, one thread each: a wait or
+//                   a commit takes about a hundred cycles of its thread even when
+//                   nothing is left to wait for, and with one thread for both
+//                   chains these, not the tensor core, set the pace (16 x 64K-128K
+//                   tokens: 1115 us)
 // TMEM (512 columns): S_A/P_A, S_B/P_B, O_A, O_B, 128 columns each; P is bf16
 // over the first 64 columns of its S.
 //
@@ -59,6 +66,7 @@ struct Smem {
     static constexpr int KB = D / 64;
     static constexpr uint32_t TILE = (uint32_t)KB * kBlk;
     static constexpr int QTILES = PAIR ? 2 : 1;
+    // stages: of K and of V (PAIR), of chain A's ring and of chain B's (ALT)
     static constexpr int KST = D == 128 ? 3 : 6;
     static constexpr int VST = (D == 128 ? 3 : 6) - (PAIR ? 1 : 0);
     static constexpr uint32_t Q = 0;
@@ -66,8 +74,8 @@ struct Smem {
     static constexpr uint32_t V = K + KST * TILE;
     static constexpr uint32_t ML = V + VST * TILE;      // float2[128]: chain B's (m, l)
     static constexpr uint32_t BAR = ML + 128 * 8;
-    static constexpr uint32_t MISC = BAR + 40 * 8;
-    static constexpr uint32_t BYTES = MISC + 128;
+    static constexpr uint32_t MISC = BAR + 48 * 8;
+    static constexpr uint32_t BYTES = MISC + 192;
     static constexpr uint32_t ALLOC = BYTES + 1024;     // alignment slack
 };
 static_assert(Smem<128, true>::ALLOC <= 232448 && Smem<128, false>::ALLOC <= 232448, "shared memory");
@@ -76,25 +84,27 @@ enum Bar {
     kQFull = 0,    // 2: Q tile loaded
     kQEmpty = 2,   // 2: last S MMA on the Q tile done
     kSFull = 4,    // 2: S of chain A / B ready
-    kPFull = 6,    // 2: P written (128 arrivals)
+    kPFull = 6,    // 2: P written (4 arrivals, one a warp)
     kODone = 8,    // 2: P.V finished
-    kOFree = 10,   // 2: O read out (128 arrivals)
-    kML = 12,      // chain B's (m, l) written (128 arrivals)
-    kDrain = 13,
-    kKFull = 14,   // up to 6 each
-    kKEmpty = 20,
-    kVFull = 26,
-    kVEmpty = 32,
-    kNumBars = 38
+    kOFree = 10,   // 2: O read out (4 arrivals)
+    kML = 12,      // chain B's (m, l) written (4 arrivals)
+    kDrain = 13,   // 2
+    kKFull = 15,   // up to 6 each; ALT: of chain A's ring
+    kKEmpty = 21,
+    kVFull = 27,   // ALT: of chain B's ring
+    kVEmpty = 33,
+    kVClean = 39,  // PAIR: chain A is done with cleaning the tile (4 arrivals)
+    kTurn = 45,    // 2: chain A's / B's turn to issue MMAs
+    kNumBars = 47
 };
 
 struct Misc {
     uint32_t tmem;
     int abort;
-    int poison[4];   // by segment mod 4: the last segment with an infinity or NaN cleared from a seen V row
+    int poison[8];   // by segment mod 8: the last segment with an infinity or NaN cleared from a seen V row
     Range range;
 };
-static_assert(sizeof(Misc) <= 128, "misc area");
+static_assert(sizeof(Misc) <= 192, "misc area");
 
 YOCO_DEV bool wait1(uint64_t *bar, uint32_t parity) { return mbar_wait(bar, parity, &g_status_tree_tc); }
 YOCO_DEV bool waitw(uint64_t *bar, uint32_t parity) {
@@ -149,6 +159,47 @@ YOCO_DEV void add_odd(const __nv_bfloat16 *v, float *o) {
     }
 }
 
+// The larger of three, NaN if any is.
+YOCO_DEV float max3_nan(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// 2^x for a pair on the FMA pipe, x <= 8 or so: x = n + f with n the nearest
+// integer (by adding 1.5 * 2^23) and f in [-1/2, 1/2] (Cody-Waite reduction),
+// 2^f by the polynomial 1 + f (c1 + f (c2 + f (c3 + f c4))), a minimax fit of the
+// relative error under p(0) = 1 (a linear program over 4001 points: 2.9e-6, mean
+// 3.4e-7), 2^n by adding n to the exponent field.  x is held at -127 at the
+// least, where f = 0, p = 1 and the exponent field comes out as zero: a masked
+// score (-inf) gives exactly 0.
+YOCO_DEV void exp2_pair(float x0, float x1, float &e0, float &e1) {
+    constexpr uint64_t kRound = tc::f2_const(0x4B400000u);  // 1.5 * 2^23
+    constexpr uint64_t kOne = tc::f2_const(0x3F800000u);
+    constexpr uint64_t kC1 = tc::f2_const(0x3F317095u);     // 0.69312412
+    constexpr uint64_t kC2 = tc::f2_const(0x3E7601C1u);     // 0.24024107
+    constexpr uint64_t kC3 = tc::f2_const(0x3D64FE8Fu);     // 0.05590683
+    constexpr uint64_t kC4 = tc::f2_const(0x3C1D003Du);     // 0.00958258
+    const uint64_t X = tc::f2_pack(fmaxf(x0, -127.f), fmaxf(x1, -127.f));
+    const uint64_t T = tc::f2_add(X, kRound);
+    const uint64_t F = tc::f2_sub(X, tc::f2_sub(T, kRound));
+    uint64_t P = tc::f2_fma(F, kC4, kC3);
+    P = tc::f2_fma(P, F, kC2);
+    P = tc::f2_fma(P, F, kC1);
+    P = tc::f2_fma(P, F, kOne);
+    float p0, p1, t0, t1;
+    tc::f2_unpack(P, p0, p1);
+    tc::f2_unpack(T, t0, t1);
+    e0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23));
+    e1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23));
+}
+
+// Of every eight pairs of columns, how many take the FMA pipe.
+#ifndef TREE_POLY
+#define TREE_POLY 2
+#endif
+constexpr int kPoly = TREE_POLY;
+
 // A ring segment's bounds over all its nodes: what every node sees and what
 // any does.
 struct RingSpan {
@@ -186,22 +237,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < 2; ++s) {
             mbar_init(&bars[kQFull + s], 1);
-            mbar_init(&bars[kQEmpty + s], 1);
+            mbar_init(&bars[kQEmpty + s], PAIR ? 1 : 2);   // ALT: both chains read the one tile
             mbar_init(&bars[kSFull + s], 1);
-            mbar_init(&bars[kPFull + s], 128);
+            mbar_init(&bars[kPFull + s], 4);
             mbar_init(&bars[kODone + s], 1);
-            mbar_init(&bars[kOFree + s], 128);
+            mbar_init(&bars[kOFree + s], 4);
+            mbar_init(&bars[kTurn + s], 1);
         }
-        mbar_init(&bars[kML], 128);
-        mbar_init(&bars[kDrain], 1);
+        mbar_init(&bars[kML], 4);
+        for (int s = 0; s < 2; ++s) mbar_init(&bars[kDrain + s], 1);
         for (int s = 0; s < 6; ++s) {
             mbar_init(&bars[kKFull + s], 1);
-            mbar_init(&bars[kKEmpty + s], 1);
+            mbar_init(&bars[kKEmpty + s], PAIR ? 2 : 1);   // PAIR: both chains read the tile
             mbar_init(&bars[kVFull + s], 1);
-            mbar_init(&bars[kVEmpty + s], 1);
+            mbar_init(&bars[kVEmpty + s], PAIR ? 2 : 1);
+            mbar_init(&bars[kVClean + s], 4);
         }
         misc->abort = 0;
-        for (int s = 0; s < 4; ++s) misc->poison[s] = -1;
+        for (int s = 0; s < 8; ++s) misc->poison[s] = -1;
         fence_mbar_init();
     }
     if (warp == 9) {
@@ -221,151 +274,160 @@ __global__ void __launch_bounds__(kThreads, 1)
     Iter it(p, misc->range);
     Seg sg;
 
-    if (warp == 8 || warp >= 10) {
+    if (warp == 8 || warp == 10) {
         // ----------------------------------------------------- TMA producers
-        if (lane == 0 && warp == 11) {
-            int k = 0;
-            for (; !*abort_flag && it.next(p, sg); ++k) {
-                bool ok = true;
-                for (int hh = 0; hh < L::QTILES; ++hh) {
-                    if (!wait1(&bars[kQEmpty + hh], (k & 1) ^ 1)) { ok = false; break; }
-                    mbar_arrive_expect_tx(&bars[kQFull + hh], 128 * D * 2);
-                    const int node0 = (sg.rt * L::QTILES + hh) * (128 >> p.lg);
-                    for (int kb = 0; kb < KB; ++kb)
-                        tc::tma_load_4d(base + L::Q + hh * L::TILE + kb * kBlk, &tm_q, kb * 64, sg.g << p.lg, node0, sg.b,
-                                        &bars[kQFull + hh]);
+        if (lane == 0) {
+            const bool one = warp == 8;                     // K / chain A
+            const bool has_q = PAIR ? !one : one;
+            const int ST = one ? L::KST : L::VST;
+            uint64_t *full = &bars[one ? kKFull : kVFull], *empty = &bars[one ? kKEmpty : kVEmpty];
+            const uint32_t dst0 = base + (one ? L::K : L::V);
+            int u = 0, k = 0;   // copies, segments whose Q is on its way
+            bool ok = true;
+            while (ok && !*abort_flag && it.next(p, sg)) {
+                if (has_q) {
+                    for (int hh = 0; hh < L::QTILES && ok; ++hh) {
+                        ok = wait1(&bars[kQEmpty + hh], (k & 1) ^ 1);
+                        if (!ok) break;
+                        mbar_arrive_expect_tx(&bars[kQFull + hh], 128 * D * 2);
+                        const int node0 = (sg.rt * L::QTILES + hh) * (128 >> p.lg);
+                        for (int kb = 0; kb < KB; ++kb)
+                            tc::tma_load_4d(base + L::Q + hh * L::TILE + kb * kBlk, &tm_q, kb * 64, sg.g << p.lg, node0,
+                                            sg.b, &bars[kQFull + hh]);
+                    }
+                    if (ok) ++k;
                 }
-                if (!ok) { *abort_flag = 1; ++k; break; }
-            }
-            // drain: the last copies issued must land before this CTA may exit
-            if (k > 0)
-                for (int hh = 0; hh < L::QTILES; ++hh)
-                    if (!wait1(&bars[kQFull + hh], (k - 1) & 1)) break;
-        } else if (lane == 0) {
-            const bool is_k = warp == 8;
-            const int ST = is_k ? L::KST : L::VST;
-            uint64_t *full = &bars[is_k ? kKFull : kVFull], *empty = &bars[is_k ? kKEmpty : kVEmpty];
-            const CUtensorMap *ctx_map = is_k ? &tm_k : &tm_v, *node_map = is_k ? &tm_kn : &tm_vn;
-            const uint32_t dst0 = base + (is_k ? L::K : L::V);
-            int u = 0;
-            while (!*abort_flag && it.next(p, sg)) {
-                for (int t = sg.t0; t < sg.t1; ++t, ++u) {
-                    const int st = u % ST;
-                    if (!wait1(&empty[st], ((u / ST) & 1) ^ 1)) { *abort_flag = 1; break; }
-                    if (*abort_flag) break;
+                for (int t = sg.t0 + (PAIR || one ? 0 : 1); ok && t < sg.t1; t += PAIR ? 1 : 2) {
                     const bool nodes = t == sg.n_ctx_tiles;
                     const int row = nodes ? 0 : RING ? t * BN : (int)(sg.row0 + (int64_t)t * BN);
                     const int b = nodes || RING ? sg.b : 0;
-                    mbar_arrive_expect_tx(&full[st], (nodes ? kTreeMaxNodes : BN) * D * 2);
-                    for (int kb = 0; kb < KB; ++kb)
-                        tc::tma_load_4d(dst0 + st * L::TILE + kb * kBlk, nodes ? node_map : ctx_map, kb * 64, sg.g, row, b,
-                                        &full[st]);
+#pragma unroll
+                    for (int e = 0; e < (PAIR ? 1 : 2) && ok; ++e) {
+                        const bool is_k = PAIR ? one : e == 0;
+                        const CUtensorMap *map = is_k ? nodes ? &tm_kn : &tm_k : nodes ? &tm_vn : &tm_v;
+                        const int st = u % ST;
+                        ok = wait1(&empty[st], ((u / ST) & 1) ^ 1);
+                        if (!ok) break;
+                        mbar_arrive_expect_tx(&full[st], (nodes ? kTreeMaxNodes : BN) * D * 2);
+                        for (int kb = 0; kb < KB; ++kb)
+                            tc::tma_load_4d(dst0 + st * L::TILE + kb * kBlk, map, kb * 64, sg.g, row, b, &full[st]);
+                        ++u;
+                    }
                 }
             }
+            if (!ok) *abort_flag = 1;
+            // drain: the last copies issued must land before this CTA may exit
             for (int q = max(0, u - ST); q < u; ++q)
                 if (!wait1(&full[q % ST], (q / ST) & 1)) break;
+            if (k > 0)
+                for (int hh = 0; hh < L::QTILES; ++hh)
+                    if (!wait1(&bars[kQFull + hh], (k - 1) & 1)) break;
         }
-    } else if (warp == 9) {
-        // ---------------------------------------------------------- MMA issue
+    } else if (warp == 9 || warp == 11) {
+        // ------------------------------------------- MMA issue of one chain
         if (lane == 0) {
+            const int hh = warp == 9 ? 0 : 1;
             constexpr uint32_t idS = tc::idesc_bf16(128, BN, false, false);
             constexpr uint32_t idPV = tc::idesc_bf16(128, D, false, true);
             // descriptors as (low, high) words: the low one holds the address and the
-            // leading offset, so a step is one 32-bit addition.  This thread's
-            // instructions between two MMAs are on every chain's critical path.
+            // leading offset, so a step is one 32-bit addition
             constexpr uint32_t kHi = (1024u >> 4) | 1u << 14 | 2u << 29;
             constexpr uint32_t kLoS = (16u >> 4) << 16, kLoV = (kBlk >> 4) << 16;
-            const uint32_t q_lo = ((base + L::Q) >> 4) | kLoS;
-            const uint32_t k_lo = ((base + L::K) >> 4) | kLoS;
-            const uint32_t v_lo = ((base + L::V) >> 4) | kLoV;
+            const uint32_t q_lo = ((base + L::Q + (PAIR ? hh * L::TILE : 0)) >> 4) | kLoS;
+            const uint32_t ts = tmem + hh * 128, to = tmem + 256 + hh * 128;
             auto desc = [](uint32_t lo) { return (uint64_t)kHi << 32 | lo; };
-            // the tile whose P.V is still owed to a chain
-            struct Owed {
-                uint32_t v_lo, v_parity, p_parity, o_parity;
-                int v_stage, seg;
-                bool any, first, wait_o, nodes;   // first: opens its segment; wait_o: not the chain's first segment
-            } owed_a = {}, owed_b = {};
-            auto issue_pv = [&](int hh, Owed &w) -> bool {
-                if (w.wait_o && !wait1(&bars[kOFree + hh], w.o_parity)) return false;
-                if (!wait1(&bars[kPFull + hh], w.p_parity)) return false;
-                if ((!PAIR || hh == 0) && !wait1(&bars[kVFull + w.v_stage], w.v_parity)) return false;
-                tc::fence_after_sync();
-                const uint32_t tp = tmem + hh * 128, to = tmem + 256 + hh * 128;
-                tc::mma_bf16_ts(to, tp, desc(w.v_lo), idPV, w.first ? 0u : 1u);
-#pragma unroll
-                for (int kk = 1; kk < kTreeMaxNodes / 16; ++kk)
-                    tc::mma_bf16_ts(to, tp + kk * 8, desc(w.v_lo + kk * (2048 >> 4)), idPV, 1u);
-                if (!w.nodes) {
-#pragma unroll
-                    for (int kk = kTreeMaxNodes / 16; kk < BN / 16; ++kk)
-                        tc::mma_bf16_ts(to, tp + kk * 8, desc(w.v_lo + kk * (2048 >> 4)), idPV, 1u);
+            uint64_t *q_full = &bars[kQFull + (PAIR ? hh : 0)], *q_empty = &bars[kQEmpty + (PAIR ? hh : 0)];
+            // PAIR: the K stages and the V stages, both chains'.  ALT: the chain's one
+            // ring in both roles
+            struct Ring {
+                uint64_t *full, *empty;
+                uint32_t addr, phase;
+                int st, n;
+                YOCO_DEV void advance() {
+                    if (++st == n) {
+                        st = 0;
+                        phase ^= 1;
+                    }
                 }
-                tc::mma_commit(&bars[kODone + hh]);
-                if (!PAIR || hh == 1) tc::mma_commit(&bars[kVEmpty + w.v_stage]);
-                w.any = false;
-                return true;
             };
+            const bool one = PAIR || hh == 0;
+            Ring rk = {&bars[one ? kKFull : kVFull], &bars[one ? kKEmpty : kVEmpty], (base + (one ? L::K : L::V)) >> 4, 0,
+                       0, L::KST};
+            Ring rv_own = {&bars[kVFull], &bars[kVEmpty], (base + L::V) >> 4, 0, 0, L::VST};
+            Ring &rv = PAIR ? rv_own : rk;
             bool ok = true;
-            int seg = 0, kst = 0, vst = 0;
-            uint32_t k_ph = 0, v_ph = 0;
-            int ga = 0, gb = 0, ka = 0, kb = 0;   // tiles and segments of chain A, B
-            // S of one chain (after the P.V it still owes), then the new debt
-            auto step = [&](int hh, Owed &w, int &g, int k, bool opens, bool last, bool nodes) -> bool {
-                if (w.any && !issue_pv(hh, w)) return false;
-                if (opens && (PAIR || hh == 0) && !wait1(&bars[kQFull + hh], seg & 1)) return false;
-                tc::fence_after_sync();
-                const uint32_t qd = q_lo + (PAIR ? hh * (L::TILE >> 4) : 0), kd = k_lo + kst * (L::TILE >> 4);
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = ((kk >> 2) * kBlk + (kk & 3) * 32) >> 4;
-                    tc::mma_bf16_ss(tmem + hh * 128, desc(qd + off), desc(kd + off), idS, kk > 0 ? 1u : 0u);
+            int seg = 0;
+            uint32_t g = 0, k = 0, turn = 0;   // the chain's tiles, segments and turns
+            for (; ok && !*abort_flag && it.next(p, sg); ++seg) {
+                const int nt = sg.t1 - sg.t0;
+                // tiles of this chain and of chain B; the node tile, if this chain has it
+                const int mine = PAIR ? nt : (nt + 1 - hh) / 2, others_b = PAIR ? nt : nt / 2;
+                const int n_ctx = sg.n_ctx_tiles - sg.t0;
+                const int n_nodes = PAIR ? n_ctx : (n_ctx & 1) == hh ? n_ctx >> 1 : -1;
+                ok = wait1(q_full, seg & 1);
+                if (!ok) break;
+                if (mine == 0) {   // nothing for this chain, which has its say on Q all the same
+                    mbar_arrive(q_empty);
+                    continue;
                 }
-                tc::mma_commit(&bars[kSFull + hh]);
-                if (last) tc::mma_commit(&bars[kQEmpty + (PAIR ? hh : 0)]);
-                if (!PAIR || hh == 1) tc::mma_commit(&bars[kKEmpty + kst]);
-                w.v_lo = v_lo + vst * (L::TILE >> 4);
-                w.v_stage = vst;
-                w.v_parity = v_ph;
-                w.p_parity = g & 1;
-                w.o_parity = (k - 1) & 1;
-                w.wait_o = opens && k >= 1;
-                w.first = opens;
-                w.nodes = nodes;
-                w.seg = seg;
-                w.any = true;
-                ++g;
-                return true;
-            };
-            for (; ok && it.next(p, sg); ++seg) {
-                const int nt = sg.t1 - sg.t0, n_ctx = sg.n_ctx_tiles - sg.t0;
-                for (int i = 0; i < nt; ++i) {
-                    if (!wait1(&bars[kKFull + kst], k_ph)) { ok = false; break; }
-                    const bool last = i == nt - 1, nodes = i == n_ctx;
-                    if (PAIR)
-                        ok = step(0, owed_a, ga, ka, i == 0, last, nodes) && step(1, owed_b, gb, kb, i == 0, last, nodes);
-                    else if (i & 1)
-                        ok = step(1, owed_b, gb, kb, i == 1, last, nodes);
-                    else
-                        ok = step(0, owed_a, ga, ka, i == 0, last, nodes);
+                // step n: P V of tile n - 1 and S of tile n, the chains in turns (A's step
+                // 0, B's step 0, A's step 1, ...), so that one chain's MMAs run under the
+                // other's softmax: unordered, the two fall into step, with the exponentials
+                // of both at once and then the MMAs of both at once
+                for (int n = 0; n <= mine; ++n) {
+                    uint32_t vd = 0;
+                    uint64_t *v_empty = nullptr;
+                    if (n > 0) {
+                        ok = wait1(&rv.full[rv.st], rv.phase) &&
+                             (!PAIR || hh == 0 || wait1(&bars[kVClean + rv.st], rv.phase)) &&
+                             (n > 1 || k == 0 || wait1(&bars[kOFree + hh], (k - 1) & 1));
+                        vd = (rv.addr + rv.st * (L::TILE >> 4)) | kLoV;
+                        v_empty = &rv.empty[rv.st];
+                        rv.advance();
+                    }
+                    ok = ok && (n == mine || wait1(&rk.full[rk.st], rk.phase));
+                    if (n > 0) ok = ok && wait1(&bars[kPFull + hh], g++ & 1);
+                    if (hh == 1 || (others_b > 0 && n > 0)) ok = ok && wait1(&bars[kTurn + hh], turn++ & 1);
                     if (!ok) break;
-                    if (++kst == L::KST) { kst = 0; k_ph ^= 1; }
-                    if (++vst == L::VST) { vst = 0; v_ph ^= 1; }
+                    tc::fence_after_sync();
+                    if (n > 0) {
+                        tc::mma_bf16_ts(to, ts, desc(vd), idPV, n > 1 ? 1u : 0u);
+#pragma unroll
+                        for (int kk = 1; kk < kTreeMaxNodes / 16; ++kk)
+                            tc::mma_bf16_ts(to, ts + kk * 8, desc(vd + kk * (2048 >> 4)), idPV, 1u);
+                        if (n - 1 != n_nodes) {
+#pragma unroll
+                            for (int kk = kTreeMaxNodes / 16; kk < BN / 16; ++kk)
+                                tc::mma_bf16_ts(to, ts + kk * 8, desc(vd + kk * (2048 >> 4)), idPV, 1u);
+                        }
+                        tc::mma_commit(v_empty);
+                    }
+                    if (n < mine) {
+                        const uint32_t kd = (rk.addr + rk.st * (L::TILE >> 4)) | kLoS;
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t off = ((kk >> 2) * kBlk + (kk & 3) * 32) >> 4;
+                            tc::mma_bf16_ss(ts, desc(q_lo + off), desc(kd + off), idS, kk > 0 ? 1u : 0u);
+                        }
+                    }
+                    if (hh == 1 || n <= others_b - (others_b == 0)) mbar_arrive(&bars[kTurn + (hh ^ 1)]);
+                    if (n < mine) {
+                        tc::mma_commit(&bars[kSFull + hh]);
+                        tc::mma_commit(&rk.empty[rk.st]);
+                        rk.advance();
+                        if (n == mine - 1) tc::mma_commit(q_empty);
+                    }
+                    if (n > 0) tc::mma_commit(&bars[kODone + hh]);
                 }
                 if (!ok) break;
-                ++ka;
-                if (PAIR || nt >= 2) ++kb;
-                // a one-tile segment leaves chain B out: what an older segment owes
-                // it cannot wait for its next tile, since chain A waits for it
-                if (!PAIR && owed_b.any && owed_b.seg < seg) ok = issue_pv(1, owed_b);
-                if (*abort_flag) ok = false;
+                // as many of chain B's turns behind chain A as it has steps
+                if (hh == 0 && others_b == mine) ok = wait1(&bars[kTurn], turn++ & 1);
+                ++k;
             }
-            // the last debts, in any order: the chains do not wait for each other here
-            if (ok && owed_a.any) ok = issue_pv(0, owed_a);
-            if (ok && owed_b.any) ok = issue_pv(1, owed_b);
             if (!ok) *abort_flag = 1;
             // every MMA issued by this thread has finished before TMEM is freed
-            tc::mma_commit(&bars[kDrain]);
-            wait1(&bars[kDrain], 0);
+            tc::mma_commit(&bars[kDrain + hh]);
+            wait1(&bars[kDrain + hh], 0);
         }
     } else {
         // ------------------------------------------------------------ softmax
@@ -446,10 +508,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!waitw(&bars[kSFull + hh], g[hh] & 1)) { ok = false; break; }
                 tc::fence_after_sync();
                 if (masked && (!PAIR || hh == 0)) {
-                    // V rows before P V: thread r has key row r.  After S(u), whose
-                    // MMAs were issued after P.V of tile u - VST: that tile's V had
-                    // landed, so the parity below cannot mean an older phase
-                    if (!waitw(&bars[kVFull + u % L::VST], (u / L::VST) & 1)) { ok = false; break; }
+                    // V rows before P V: thread r has key row r.  After S of this tile,
+                    // which was issued after the stage's last tenant had landed, so the
+                    // parity below cannot mean an older phase
+                    const int at = PAIR ? u : 2 * g[hh] + 1;   // copies before it in its ring
+                    const int vst = PAIR || hh == 1 ? L::VST : L::KST, v0 = PAIR || hh == 1 ? kVFull : kKFull;
+                    if (!waitw(&bars[v0 + at % vst], (at / vst) & 1)) { ok = false; break; }
                     bool unseen, whole_row = false;
                     if (nodes) {
                         unseen = r >= sg.n;
@@ -463,10 +527,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         whole_row = !unseen;   // every row sees it: what it holds counts for all
                     }
                     if (!whole_row && !(nodes && r >= kTreeMaxNodes)) {
-                        if (clean_v_row<KB>(sbase + L::V + (u % L::VST) * L::TILE, r, unseen))
-                            *(volatile int *)&misc->poison[seg & 3] = seg;
+                        if (clean_v_row<KB>(sbase + (PAIR || hh == 1 ? L::V : L::K) + (at % vst) * L::TILE, r, unseen))
+                            *(volatile int *)&misc->poison[seg & 7] = seg;
                         fence_proxy_async_smem();
                     }
+                }
+                if (PAIR && hh == 0) {
+                    // chain B's P V reads this tile too
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars[kVClean + u % L::VST]);
                 }
                 if (active) {
                     float s[BN];
@@ -504,16 +573,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     float a8[8];
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk) a8[kk] = tc::max3(s[kk], s[kk + 8], s[kk + 16]);
+                    for (int kk = 0; kk < 8; ++kk) a8[kk] = max3_nan(s[kk], s[kk + 8], s[kk + 16]);
 #pragma unroll
                     for (int c = 24; c < 120; c += 16)
 #pragma unroll
-                        for (int kk = 0; kk < 8; ++kk) a8[kk] = tc::max3(a8[kk], s[c + kk], s[c + 8 + kk]);
+                        for (int kk = 0; kk < 8; ++kk) a8[kk] = max3_nan(a8[kk], s[c + kk], s[c + 8 + kk]);
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk) a8[kk] = fmaxf(a8[kk], s[120 + kk]);
-                    const float mx = tc::max3(tc::max3(a8[0], a8[1], a8[2]), tc::max3(a8[3], a8[4], a8[5]),
-                                              fmaxf(a8[6], a8[7]));
-                    // the reference moves (and O is rescaled) only when it grows by more than 2^8
+                    for (int kk = 0; kk < 8; ++kk) a8[kk] = max3_nan(a8[kk], a8[kk], s[120 + kk]);
+                    const float mx = max3_nan(max3_nan(a8[0], a8[1], a8[2]), max3_nan(a8[3], a8[4], a8[5]),
+                                              max3_nan(a8[6], a8[6], a8[7]));
+                    // the reference moves (and O is rescaled) only when it grows by more than
+                    // 2^8; a NaN or +inf score makes it NaN, and with it the row
                     const float m_cand = mx * p.scale_log2;
                     float alpha = 1.f;
                     const bool grow = m_cand > m + 8.f;
@@ -521,6 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         alpha = m == -INFINITY ? 0.f : tc::ex2(m - m_cand);
                         m = m_cand;
                     }
+                    if (!(mx < INFINITY)) m = NAN;
                     const float neg_m = m == -INFINITY ? 0.f : -m;
                     const uint64_t nm2 = tc::f2_pack(neg_m, neg_m);
                     uint64_t rs2a = 0, rs2b = 0;
@@ -532,7 +603,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const int c = half * (BN / 2) + cc;
                             float x0, x1;
                             tc::f2_unpack(tc::f2_fma(tc::f2_pack(s[c], s[c + 1]), sl2, nm2), x0, x1);
-                            const float e0 = tc::ex2(x0), e1 = tc::ex2(x1);
+                            float e0, e1;
+                            if ((c >> 1) * kPoly % 8 < kPoly) {
+                                exp2_pair(x0, x1, e0, e1);
+                            } else {
+                                e0 = tc::ex2(x0);
+                                e1 = tc::ex2(x1);
+                            }
                             if (c & 2)
                                 rs2b = tc::f2_add(rs2b, tc::f2_pack(e0, e1));
                             else
@@ -564,7 +641,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 first = false;
                 tc::fence_before_sync();
-                mbar_arrive(&bars[kPFull + hh]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[kPFull + hh]);
                 ++g[hh];
             }
             if (!ok) break;
@@ -574,7 +652,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (has_b) {
                     if (k[1] >= 1 && !waitw(&bars[kOFree + 1], (k[1] - 1) & 1)) { ok = false; break; }
                     s_ml[r] = make_float2(m, l);
-                    mbar_arrive(&bars[kML]);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars[kML]);
                 }
                 ++k[0];
                 k[1] += has_b;
@@ -594,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 m = mm;
             }
             tc::fence_after_sync();
-            const bool poison = *(volatile int *)&misc->poison[seg & 3] == seg;
+            const bool poison = *(volatile int *)&misc->poison[seg & 7] == seg;
             const bool none = m == -INFINITY && l == 0.f;   // a NaN sum is not nothing
             const float inv = none ? 0.f : 1.f / l;
             const int head = (sg.g << p.lg) + (row & ((1 << p.lg) - 1));
@@ -650,8 +729,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             tc::fence_before_sync();
-            mbar_arrive(&bars[kOFree + hh]);
-            if (join) mbar_arrive(&bars[kOFree + 1]);
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&bars[kOFree + hh]);
+                if (join) mbar_arrive(&bars[kOFree + 1]);
+            }
             if (live && sg.whole && p.lse)
                 p.lse[((int64_t)sg.b * p.Hq + head) * p.N + node] = none ? -INFINITY : (m + __log2f(l)) * kLn2;
             if (live && !sg.whole) p.ws_ml[entry * RS + ws_row] = make_float2(m, l);
