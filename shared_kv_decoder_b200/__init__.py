@@ -465,27 +465,29 @@ def debug_exp2_poly(x, y=None):
 
 
 # ---------------------------------------------- rotary positions, drafted tokens
-def _want(t, name, dtypes, shape, device):
-    """One tensor argument: its type, shape, device and layout."""
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name}: {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
+def _want(t, name, dtype, shape, device):
+    """One tensor argument: its type, shape, device (an index) and layout."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return
+    if t.dtype is not dtype:
+        raise ValueError(f"{name}: {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if not t.is_contiguous():
-        raise ValueError("libyoco takes contiguous tensors only")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
+    raise ValueError("libyoco takes contiguous tensors only")
 
 
 def _cuda_float(t, name):
+    """The device index of the tensor that the others go by."""
     if not t.is_cuda:
         raise ValueError("libyoco takes CUDA tensors only")
     if t.dtype not in _DT:
         raise ValueError(f"{name}: {t.dtype}, expected {' or '.join(str(d) for d in _DT)}")
-    return t.device
+    return t.get_device()
 
 
-_I32, _I64, _MASK = (torch.int32,), (torch.int64,), (torch.int64, torch.uint64)
+_I32, _I64 = torch.int32, torch.int64
 
 
 @functools.lru_cache(maxsize=256)
@@ -498,13 +500,13 @@ def _addr(t):
 
 
 def _call(device, name, *args):
-    """A library call on `device` and its current stream."""
-    fn = getattr(load(), name)
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    """A library call on CUDA device `device` and its current stream."""
+    fn = getattr(_LIB or load(), name)
+    if device == torch.cuda.current_device():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(device))
     else:
-        status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+        with torch.cuda.device(device):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(device))
     if status != OK:
         raise YocoError(status, name)
 
@@ -534,27 +536,37 @@ def rope(q, k, rope_cfg, pos=None, pos0=0, q_out=None, k_out=None, backward=Fals
     if x is None:
         raise ValueError("rope needs q or k")
     device = _cuda_float(x, "q" if q is not None else "k")
-    lead = x.shape[:-2]
-    if len(lead) not in (1, 2):
+    dtype, shape = x.dtype, x.shape
+    if len(shape) == 4:
+        B, T, Hq, D = shape
+        lead = (B, T)
+    elif len(shape) == 3:
+        B, Hq, D = shape
+        T, lead = 1, (B,)
+    else:
         raise ValueError("rope takes [B, T, heads, D] or [B, heads, D]")
-    B, T = lead if len(lead) == 2 else (lead[0], 1)
-    D = x.shape[-1]
-    Hq = Hkv = x.shape[-2]
+    Hkv = Hq
     if q is not None:
-        _want(q, "q", (x.dtype,), (*lead, Hq, D), device)
-        q_out = torch.empty_like(q) if q_out is None else q_out
-        _want(q_out, "q_out", (x.dtype,), q.shape, device)
+        _want(q, "q", dtype, shape, device)
+        if q_out is None:
+            q_out = torch.empty_like(q)
+        elif q_out is not q:
+            _want(q_out, "q_out", dtype, shape, device)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
     if k is not None:
-        Hkv = k.shape[-2]
-        _want(k, "k", (x.dtype,), (*lead, Hkv, D), device)
-        k_out = torch.empty_like(k) if k_out is None else k_out
-        _want(k_out, "k_out", (x.dtype,), k.shape, device)
-    if (q is None) != (q_out is None) or (k is None) != (k_out is None):
-        raise ValueError("an output without its input")
+        Hkv = k.shape[-2] if k.dim() == len(shape) else -1
+        _want(k, "k", dtype, (*lead, Hkv, D), device)
+        if k_out is None:
+            k_out = torch.empty_like(k)
+        elif k_out is not k:
+            _want(k_out, "k_out", dtype, k.shape, device)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
     if pos is not None:
         _want(pos, "pos", _I64, lead, device)
     _call(device, "yoco_rope", _addr(q), _addr(k), B, T, _addr(pos), int(pos0), int(bool(backward)), _addr(q_out),
-          _addr(k_out), ctypes.byref(rope_cfg), _cfg_ref(Hq, Hkv, D, x.dtype))
+          _addr(k_out), ctypes.byref(rope_cfg), _cfg_ref(Hq, Hkv, D, dtype))
     return q_out, k_out
 
 
@@ -573,31 +585,35 @@ def swa_decode_tree_workspace_size(B, N, window, Hq, Hkv, D, dtype):
 
 
 def _tree_args(q, k_nodes, v_nodes, tree_mask, n_nodes, context, workspace, o, want_lse):
-    """What both trees check and allocate: (B, N, Hkv, device, workspace, o, lse)."""
+    """What both trees check and allocate.  The workspace itself comes last, to be
+    kept until the call is on its stream."""
     device = _cuda_float(q, "q")
     if q.dim() != 4 or k_nodes.dim() != 4:
         raise ValueError("q is [B, N, Hq, D], k_nodes and v_nodes [B, N, Hkv, D]")
-    B, N, Hq, D = q.shape
+    dtype, shape = q.dtype, q.shape
+    B, N, Hq, D = shape
     Hkv = k_nodes.shape[2]
-    own = (q.dtype,)
-    _want(q, "q", own, q.shape, device)
-    _want(k_nodes, "k_nodes", own, (B, N, Hkv, D), device)
-    _want(v_nodes, "v_nodes", own, (B, N, Hkv, D), device)
+    nodes = (B, N, Hkv, D)
+    _want(q, "q", dtype, shape, device)
+    _want(k_nodes, "k_nodes", dtype, nodes, device)
+    _want(v_nodes, "v_nodes", dtype, nodes, device)
     if tree_mask is not None:
-        _want(tree_mask, "tree_mask", _MASK, (B, N), device)
+        _want(tree_mask, "tree_mask", torch.uint64 if tree_mask.dtype is torch.uint64 else _I64, (B, N), device)
     if n_nodes is not None:
         _want(n_nodes, "n_nodes", _I32, (B,), device)
     if workspace is None:
-        workspace = torch.empty(_tree_ws(device.index, B, N, context, Hq, Hkv, D, q.dtype), dtype=torch.uint8,
-                                device=device)
-    elif workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace: a contiguous tensor on {device}")
+        ws_bytes = _tree_ws(device, B, N, context, Hq, Hkv, D, dtype)
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace: a contiguous tensor on cuda:{device}")
+    else:
+        ws_bytes = workspace.numel() * workspace.element_size()
     if o is None:
         o = torch.empty_like(q)
     else:
-        _want(o, "o", own, q.shape, device)
-    lse = torch.empty((B, Hq, N), dtype=torch.float32, device=device) if want_lse else None
-    return B, N, Hq, Hkv, D, device, workspace, o, lse
+        _want(o, "o", dtype, shape, device)
+    lse = torch.empty((B, Hq, N), dtype=torch.float32, device=q.device) if want_lse else None
+    return B, N, Hq, Hkv, D, device, workspace.data_ptr(), ws_bytes, o, lse, workspace
 
 
 def cross_decode_tree(q, k_nodes, v_nodes, k_cache, v_cache, seq_start, seq_len, max_len, tree_mask=None,
@@ -607,17 +623,17 @@ def cross_decode_tree(q, k_nodes, v_nodes, k_cache, v_cache, seq_start, seq_len,
     seq_len int32 [B] (committed tokens); tree_mask int64 / uint64 [B, N]: bit j
     lets node i see node j (None: a chain); n_nodes int32 [B] or None (N).
     Returns o (and lse [B, Hq, N] when want_lse)."""
-    B, N, Hq, Hkv, D, device, workspace, o, lse = _tree_args(q, k_nodes, v_nodes, tree_mask, n_nodes, int(max_len),
-                                                             workspace, o, want_lse)
+    max_len, dtype = int(max_len), q.dtype
+    B, N, Hq, Hkv, D, device, ws, ws_bytes, o, lse, keep = _tree_args(q, k_nodes, v_nodes, tree_mask, n_nodes, max_len,
+                                                                      workspace, o, want_lse)
     rows = (k_cache.shape[0], Hkv, D)
-    _want(k_cache, "k_cache", (q.dtype,), rows, device)
-    _want(v_cache, "v_cache", (q.dtype,), rows, device)
+    _want(k_cache, "k_cache", dtype, rows, device)
+    _want(v_cache, "v_cache", dtype, rows, device)
     _want(seq_start, "seq_start", _I64, (B,), device)
     _want(seq_len, "seq_len", _I32, (B,), device)
     _call(device, "yoco_cross_decode_tree", q.data_ptr(), k_nodes.data_ptr(), v_nodes.data_ptr(), k_cache.data_ptr(),
           v_cache.data_ptr(), rows[0], seq_start.data_ptr(), seq_len.data_ptr(), _addr(tree_mask), _addr(n_nodes), B, N,
-          int(max_len), o.data_ptr(), _addr(lse), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-          _cfg_ref(Hq, Hkv, D, q.dtype, float(scale)))
+          max_len, o.data_ptr(), _addr(lse), ws, ws_bytes, _cfg_ref(Hq, Hkv, D, dtype, float(scale)))
     return (o, lse) if want_lse else o
 
 
@@ -626,17 +642,17 @@ def swa_decode_tree(q, k_nodes, v_nodes, node_pos, ring_k, ring_v, slot_pos, win
     """Attention of drafted tokens over the sliding-window ring, which is only
     read.  node_pos int64 [B, N]; ring_k, ring_v [B, window, Hkv, D]; slot_pos
     int32 [B, window]; the rest as in cross_decode_tree."""
-    W = int(window)
-    B, N, Hq, Hkv, D, device, workspace, o, lse = _tree_args(q, k_nodes, v_nodes, tree_mask, n_nodes, W, workspace, o,
-                                                             want_lse)
+    W, dtype = int(window), q.dtype
+    B, N, Hq, Hkv, D, device, ws, ws_bytes, o, lse, keep = _tree_args(q, k_nodes, v_nodes, tree_mask, n_nodes, W,
+                                                                      workspace, o, want_lse)
+    ring = (B, W, Hkv, D)
     _want(node_pos, "node_pos", _I64, (B, N), device)
-    _want(ring_k, "ring_k", (q.dtype,), (B, W, Hkv, D), device)
-    _want(ring_v, "ring_v", (q.dtype,), (B, W, Hkv, D), device)
+    _want(ring_k, "ring_k", dtype, ring, device)
+    _want(ring_v, "ring_v", dtype, ring, device)
     _want(slot_pos, "slot_pos", _I32, (B, W), device)
     _call(device, "yoco_swa_decode_tree", q.data_ptr(), k_nodes.data_ptr(), v_nodes.data_ptr(), node_pos.data_ptr(),
           _addr(tree_mask), _addr(n_nodes), B, N, W, ring_k.data_ptr(), ring_v.data_ptr(), slot_pos.data_ptr(),
-          o.data_ptr(), _addr(lse), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-          _cfg_ref(Hq, Hkv, D, q.dtype, float(scale)))
+          o.data_ptr(), _addr(lse), ws, ws_bytes, _cfg_ref(Hq, Hkv, D, dtype, float(scale)))
     return (o, lse) if want_lse else o
 
 
@@ -645,8 +661,8 @@ def _commit_args(k_nodes, v_nodes, path, n_path):
     if k_nodes.dim() != 4:
         raise ValueError("k_nodes and v_nodes are [B, N, Hkv, D]")
     B, N = k_nodes.shape[:2]
-    _want(k_nodes, "k_nodes", (k_nodes.dtype,), k_nodes.shape, device)
-    _want(v_nodes, "v_nodes", (k_nodes.dtype,), k_nodes.shape, device)
+    _want(k_nodes, "k_nodes", k_nodes.dtype, k_nodes.shape, device)
+    _want(v_nodes, "v_nodes", k_nodes.dtype, k_nodes.shape, device)
     _want(path, "path", _I32, (B, N), device)
     _want(n_path, "n_path", _I32, (B,), device)
     return (*k_nodes.shape, device)
@@ -658,8 +674,8 @@ def cross_tree_commit(k_nodes, v_nodes, path, n_path, k_cache, v_cache, seq_star
     Returns new_len int32 [B]; seq_len stays as it is."""
     B, N, Hkv, D, device = _commit_args(k_nodes, v_nodes, path, n_path)
     rows = (k_cache.shape[0], Hkv, D)
-    _want(k_cache, "k_cache", (k_nodes.dtype,), rows, device)
-    _want(v_cache, "v_cache", (k_nodes.dtype,), rows, device)
+    _want(k_cache, "k_cache", k_nodes.dtype, rows, device)
+    _want(v_cache, "v_cache", k_nodes.dtype, rows, device)
     _want(seq_start, "seq_start", _I64, (B,), device)
     _want(seq_len, "seq_len", _I32, (B,), device)
     if seq_cap is not None:
@@ -680,8 +696,8 @@ def swa_tree_commit(k_nodes, v_nodes, node_pos, path, n_path, ring_k, ring_v, sl
     B, N, Hkv, D, device = _commit_args(k_nodes, v_nodes, path, n_path)
     W = int(window)
     _want(node_pos, "node_pos", _I64, (B, N), device)
-    _want(ring_k, "ring_k", (k_nodes.dtype,), (B, W, Hkv, D), device)
-    _want(ring_v, "ring_v", (k_nodes.dtype,), (B, W, Hkv, D), device)
+    _want(ring_k, "ring_k", k_nodes.dtype, (B, W, Hkv, D), device)
+    _want(ring_v, "ring_v", k_nodes.dtype, (B, W, Hkv, D), device)
     _want(slot_pos, "slot_pos", _I32, (B, W), device)
     _call(device, "yoco_swa_tree_commit", k_nodes.data_ptr(), v_nodes.data_ptr(), node_pos.data_ptr(), path.data_ptr(),
           n_path.data_ptr(), B, N, W, ring_k.data_ptr(), ring_v.data_ptr(), slot_pos.data_ptr(),

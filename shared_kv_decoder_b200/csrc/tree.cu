@@ -17,9 +17,7 @@
 
 namespace yoco {
 
-// Bit 1: a sequence's arguments were out of range.
 static __device__ unsigned int g_status_tree;
-constexpr unsigned int kStatusBadSequence = 2u;
 
 namespace tree {
 namespace {
@@ -58,6 +56,7 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_co
     pdl_wait();
     if (threadIdx.x < 32) find_range<RING, RS, BN>(p, &s_range);
     __syncthreads();
+    fill_rows_without_node<T, D, RING, RS, BN>(p, threadIdx.x / 32, kSimtThreads / 32, &g_status_tree);
     const int G = 1 << p.lg;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     SegIter<RING, RS, BN> it(p, s_range);
@@ -236,80 +235,87 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_co
     }
 }
 
-// Joins the partials of shared streams; also writes the rows without a node
-// (and every row of a sequence out of range, which it reports): o = 0, lse =
-// -inf.  D / 4 lanes have four columns each of one (sequence, node, query
-// head).  SPLIT warps share a row's partials: four where there are few rows, so
-// that a long stream's partials are all in flight at once.
+// Joins the partials of shared streams.  grid.x: a block of rows; grid.y: a
+// candidate stream of a head block -- every stream, or, where there are more
+// streams than shares, the one that share grid.y + 1 starts inside of (the first
+// of its shares to do so); grid.z: the head in its block.  D / 4 lanes have four
+// columns each of one row.  SPLIT warps share a row's partials: four where there
+// are few rows, so that a long stream's partials are all in flight at once.
 template <typename T, int D, bool RING, int RS, int BN, int SPLIT>
-__global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const __grid_constant__ Params p, const int by_stream) {
     constexpr int LANES = D / 4, AHEAD = 4, ROWS = 32 * kMergeWarps / (LANES * SPLIT);
     __shared__ float s_ml[SPLIT][ROWS][2];
     __shared__ float4 s_o[SPLIT][ROWS][SPLIT > 1 ? LANES : 1];
     const int sub = threadIdx.x % LANES, slot = threadIdx.x / LANES % ROWS, share = threadIdx.x / (LANES * ROWS);
-    const int row = (int)blockIdx.x * ROWS + slot;
-    const bool real = row < p.B * p.N * p.Hq;
-    const int bn = row / p.Hq, h = row - bn * p.Hq;
-    const int b = real ? bn / p.N : 0, node = bn - b * p.N;
+    const int r = (int)blockIdx.x * ROWS + slot, blocks = p.Hkv / p.heads;
     pdl_trigger();
     pdl_wait();
-    const int T_all = p.prefix[p.B], part = p.prefix[p.B + 1], base = p.prefix[b];
+    const int T_all = p.prefix[p.B], part = p.prefix[p.B + 1];
+    const Deal d(T_all, max(1, min(T_all, p.groups)));
+    int b, stream = 0, x = 0;
+    if (by_stream) {
+        const int per_b = ((p.N << p.lg) + RS - 1) / RS * blocks;
+        b = (int)blockIdx.y / per_b;
+        stream = (int)blockIdx.y - b * per_b;
+    } else {
+        const int c = (int)blockIdx.y + 1;
+        x = part > 0 ? c * part : c < min(T_all, p.groups) ? d.start(c) : T_all;
+        if (x >= T_all) return;
+        // the sequence with tile x: the last one that starts at or before it and has tiles
+        int lo = 0, hi = p.B;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (p.prefix[mid] <= x) lo = mid;
+            else hi = mid;
+        }
+        b = lo;
+    }
+    const int base = p.prefix[b];
     const Seq s = sequence<RING, RS, BN>(p, b);
+    const int nt = s.n_ctx_tiles + 1, numbered = s.numbered(part);
+    if (!by_stream) stream = (x - base) / numbered;
+    if (stream >= s.streams(p)) return;
+    const int a = base + stream * numbered;
+    const int c0 = part > 0 ? a / part : d.owner(a), c1 = part > 0 ? (a + nt - 1) / part : d.owner(a + nt - 1);
+    if (c0 == c1 || (!by_stream && c0 != (int)blockIdx.y)) return;   // finished by its CTA; another share's
+    // the stream's part in c0 opens c0's share only when it starts there
+    const int first = part > 0 || d.start(c0) == a ? 0 : 1, n_part = c1 - c0 + 1;
+    const int g = stream % blocks * p.heads + (int)blockIdx.z, rr = stream / blocks * RS + r;
+    const int node = rr >> p.lg, h = (g << p.lg) + (rr & ((1 << p.lg) - 1));
+    bool write = r < RS && node < s.n;
+    auto entry = [&](int i) { return (int64_t)((c0 + i) * p.heads + (int)blockIdx.z) * 2 + (i == 0 ? first : 0); };
     float M = -INFINITY, L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    bool write = real;
-    if (real && node < s.n) {
-        const int g = h >> p.lg, rr = (node << p.lg) + (h & ((1 << p.lg) - 1));
-        const int nt = s.n_ctx_tiles + 1;
-        const int a = base + (rr / RS * (p.Hkv / p.heads) + g / p.heads) * s.numbered(part);
-        int c0, c1, first = 0;
-        if (part > 0) {
-            c0 = a / part;
-            c1 = (a + nt - 1) / part;
-        } else {
-            const Deal d(T_all, min(T_all, p.groups));
-            c0 = d.owner(a);
-            c1 = d.owner(a + nt - 1);
-            // the stream's part in c0 opens c0's share only when it starts there
-            first = d.start(c0) == a ? 0 : 1;
-        }
-        const int n_part = c1 - c0 + 1;
-        write = n_part > 1;   // else finished by its CTA
-        auto entry = [&](int i) { return (int64_t)((c0 + i) * p.heads + g % p.heads) * 2 + (i == 0 ? first : 0); };
-        const int r = rr % RS;
-        for (int i0 = share; write && i0 < n_part; i0 += AHEAD * SPLIT) {
-            float2 ml[AHEAD];
-            float4 o[AHEAD];
+    for (int i0 = share; write && i0 < n_part; i0 += AHEAD * SPLIT) {
+        float2 ml[AHEAD];
+        float4 o[AHEAD];
 #pragma unroll
-            for (int u = 0; u < AHEAD; ++u) {
-                ml[u] = make_float2(-INFINITY, 0.f);
-                o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (i0 + u * SPLIT < n_part) {
-                    const int64_t e = entry(i0 + u * SPLIT);
-                    ml[u] = p.ws_ml[e * RS + r];
-                    o[u] = p.ws_o[(e * LANES + sub) * RS + r];
-                }
+        for (int u = 0; u < AHEAD; ++u) {
+            ml[u] = make_float2(-INFINITY, 0.f);
+            o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i0 + u * SPLIT < n_part) {
+                const int64_t e = entry(i0 + u * SPLIT);
+                ml[u] = p.ws_ml[e * RS + r];
+                o[u] = p.ws_o[(e * LANES + sub) * RS + r];
             }
-            float mx = M;
-#pragma unroll
-            for (int u = 0; u < AHEAD; ++u) mx = fmaxf(mx, ml[u].x);
-            const float ref = mx == -INFINITY ? 0.f : mx;
-            const float keep = exp2f(M - ref);
-            L *= keep;
-            acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
-#pragma unroll
-            for (int u = 0; u < AHEAD; ++u) {
-                const float w = exp2f(ml[u].x - ref);
-                L = fmaf(w, ml[u].y, L);
-                acc.x = fmaf(w, o[u].x, acc.x);
-                acc.y = fmaf(w, o[u].y, acc.y);
-                acc.z = fmaf(w, o[u].z, acc.z);
-                acc.w = fmaf(w, o[u].w, acc.w);
-            }
-            M = mx;
         }
-    } else if (real && !s.ok && node == 0 && h == 0 && sub == 0 && share == 0) {
-        atomicOr(&g_status_tree, kStatusBadSequence);
+        float mx = M;
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) mx = fmaxf(mx, ml[u].x);
+        const float ref = mx == -INFINITY ? 0.f : mx;
+        const float keep = exp2f(M - ref);
+        L *= keep;
+        acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+            const float w = exp2f(ml[u].x - ref);
+            L = fmaf(w, ml[u].y, L);
+            acc.x = fmaf(w, o[u].x, acc.x);
+            acc.y = fmaf(w, o[u].y, acc.y);
+            acc.z = fmaf(w, o[u].z, acc.z);
+            acc.w = fmaf(w, o[u].w, acc.w);
+        }
+        M = mx;
     }
     if constexpr (SPLIT > 1) {
         if (sub == 0) {
@@ -338,7 +344,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const __gr
     if (!write) return;
     const bool none = M == -INFINITY && L == 0.f;
     const float inv = none ? 0.f : 1.f / L;
-    T *dst = static_cast<T *>(p.o) + (int64_t)row * D + 4 * sub;
+    T *dst = static_cast<T *>(p.o) + (((int64_t)b * p.N + node) * p.Hq + h) * D + 4 * sub;
     const float v[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
 #pragma unroll
     for (int e = 0; e < 4; ++e) dst[e] = from_f32<T>(v[e]);
@@ -361,12 +367,17 @@ cudaError_t launch_simt(const TreeArgs &a, const TreePlan &pl, cudaStream_t st) 
 
 template <typename T, int D, bool RING, int RS, int BN>
 cudaError_t launch_merge(const TreeArgs &a, const TreePlan &pl, cudaStream_t st) {
-    const int64_t rows = (int64_t)a.B * a.N * a.Hq;
-    const bool few = rows <= kFewRows;
+    const int rows = std::min(RS, a.N * (a.Hq / a.Hkv));
+    const int64_t streams = (int64_t)a.B * ((a.N * (a.Hq / a.Hkv) + RS - 1) / RS) * (a.Hkv / pl.heads);
+    const bool by_stream = streams <= pl.groups - 1;
+    const int most = by_stream ? (int)streams : pl.groups - 1;   // shared streams of a head
+    if (most == 0) return cudaSuccess;                           // one share: nothing to join
+    const bool few = (int64_t)rows * most * pl.heads <= kFewRows;
     const int per_cta = 32 * kMergeWarps / (D / 4) / (few ? 4 : 1);
     note_launches(1);
     return launch_pdl(few ? tree_merge_kernel<T, D, RING, RS, BN, 4> : tree_merge_kernel<T, D, RING, RS, BN, 1>,
-                      dim3((unsigned)((rows + per_cta - 1) / per_cta)), dim3(32 * kMergeWarps), 0, st, make_params(a, pl));
+                      dim3((unsigned)((rows + per_cta - 1) / per_cta), (unsigned)most, (unsigned)pl.heads),
+                      dim3(32 * kMergeWarps), 0, st, make_params(a, pl), (int)by_stream);
 }
 
 template <int D, bool RING>

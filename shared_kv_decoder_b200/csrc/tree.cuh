@@ -226,6 +226,27 @@ struct SegIter {
     }
 };
 
+// Rows without a node, and every row of a sequence out of range (which is
+// reported as bit 1 of *status): o = 0, lse = -inf.  Warp w of `warps` of every
+// CTA takes its share of the (sequence, node) pairs.
+constexpr unsigned int kStatusBadSequence = 2u;
+
+template <typename T, int D, bool RING, int RS, int BN>
+YOCO_DEV void fill_rows_without_node(const Params &p, int w, int warps, unsigned int *status) {
+    if (RING && !p.n_nodes) return;   // every node is there
+    const int lane = threadIdx.x & 31, pairs = p.B * p.N;
+    for (int i = (int)blockIdx.x * warps + w; i < pairs; i += (int)gridDim.x * warps) {
+        const int b = i / p.N, node = i - b * p.N;
+        const Seq s = sequence<RING, RS, BN>(p, b);
+        if (!s.ok && node == 0 && lane == 0) atomicOr(status, kStatusBadSequence);
+        if (node < s.n) continue;
+        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(p.o) + (int64_t)i * p.Hq * D);
+        for (int c = lane; c < p.Hq * D * (int)sizeof(T) / 16; c += 32) dst[c] = make_uint4(0, 0, 0, 0);
+        if (p.lse)
+            for (int h = lane; h < p.Hq; h += 32) p.lse[((int64_t)b * p.Hq + h) * p.N + node] = -INFINITY;
+    }
+}
+
 // ------------------------------------------------------------- visibility
 // The nodes that node i of n sees, one bit each: the mask's (a chain's without
 // one), of those that exist, and for a ring those inside i's window.

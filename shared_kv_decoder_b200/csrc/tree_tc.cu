@@ -51,6 +51,7 @@
 
 namespace yoco {
 
+// Bit 0: a bounded wait gave up; bit 1: a sequence's arguments were out of range.
 static __device__ unsigned int g_status_tree_tc;
 
 namespace tree {
@@ -119,32 +120,41 @@ YOCO_DEV uint32_t clear_odd(uint32_t w) {
     return w & ~((t >> 15 & 1u) * 0xffffu | (t >> 31) * 0xffff0000u);
 }
 
-// Key row r of a V tile: cleared whole (unseen), or of its infinities and NaN;
-// true when there were any of those.  Chunks by the swizzle's order, which
-// keeps a quarter-warp off one bank group.
-template <int KB>
-YOCO_DEV bool clean_v_row(uint8_t *tile, int r, bool unseen) {
+// Chunks [c0, c0 + NC) of each 64-column block of key row r of a V tile: cleared
+// (unseen), or cleared of its infinities and NaN; true when there were any of
+// those.  Chunks by the swizzle's order, which keeps a quarter-warp off one bank
+// group.
+template <int KB, int NC>
+YOCO_DEV bool clean_v_row(uint8_t *tile, int r, int c0, bool unseen) {
     uint8_t *row = tile + r * 128;
+    auto at = [&](int i) {
+        return reinterpret_cast<uint4 *>(row + i / NC * kBlk + (((c0 + i % NC) ^ (r & 7)) << 4));
+    };
     if (unseen) {
 #pragma unroll
-        for (int c = 0; c < 8 * KB; ++c)
-            *reinterpret_cast<uint4 *>(row + (c >> 3) * kBlk + (((c & 7) ^ (r & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < NC * KB; ++i) *at(i) = make_uint4(0, 0, 0, 0);
         return false;
     }
     uint32_t odd = 0;
 #pragma unroll
-    for (int c = 0; c < 8 * KB; ++c) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(row + (c >> 3) * kBlk + (((c & 7) ^ (r & 7)) << 4));
+    for (int i = 0; i < NC * KB; ++i) {
+        const uint4 v = *at(i);
         odd |= odd_bits(v.x) | odd_bits(v.y) | odd_bits(v.z) | odd_bits(v.w);
     }
     if (odd) {
-        for (int c = 0; c < 8 * KB; ++c) {
-            uint4 *at = reinterpret_cast<uint4 *>(row + (c >> 3) * kBlk + (((c & 7) ^ (r & 7)) << 4));
-            const uint4 v = *at;
-            *at = make_uint4(clear_odd(v.x), clear_odd(v.y), clear_odd(v.z), clear_odd(v.w));
+        for (int i = 0; i < NC * KB; ++i) {
+            const uint4 v = *at(i);
+            *at(i) = make_uint4(clear_odd(v.x), clear_odd(v.y), clear_odd(v.z), clear_odd(v.w));
         }
     }
     return odd != 0;
+}
+
+// 32-byte global store, not kept in L1; the address a multiple of 32.
+YOCO_DEV void st_global_32B(void *p, const uint32_t (&w)[8]) {
+    asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
 }
 
 // The infinities and NaN of one seen V row, added to 32 columns of its output.
@@ -265,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 8) {
         find_range<RING, RS, BN>(p, &misc->range);
         // once any CTA has recorded a timeout, the rest of the grid does nothing
-        if (lane == 0 && *(volatile unsigned int *)&g_status_tree_tc) misc->range.x = misc->range.end;
+        if (lane == 0 && *(volatile unsigned int *)&g_status_tree_tc & 1u) misc->range.x = misc->range.end;
     }
     tc::fence_before_sync();
     __syncthreads();
@@ -276,13 +286,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == 8 || warp == 10) {
         // ----------------------------------------------------- TMA producers
+        const bool one = warp == 8;                     // K / chain A
+        const int ST = one ? L::KST : L::VST;
+        uint64_t *full = &bars[one ? kKFull : kVFull], *empty = &bars[one ? kKEmpty : kVEmpty];
+        int u = 0, k = 0;   // copies, segments whose Q is on its way
         if (lane == 0) {
-            const bool one = warp == 8;                     // K / chain A
             const bool has_q = PAIR ? !one : one;
-            const int ST = one ? L::KST : L::VST;
-            uint64_t *full = &bars[one ? kKFull : kVFull], *empty = &bars[one ? kKEmpty : kVEmpty];
             const uint32_t dst0 = base + (one ? L::K : L::V);
-            int u = 0, k = 0;   // copies, segments whose Q is on its way
             bool ok = true;
             while (ok && !*abort_flag && it.next(p, sg)) {
                 if (has_q) {
@@ -316,6 +326,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (!ok) *abort_flag = 1;
+        }
+        __syncwarp();
+        // with every copy issued, these warps have time
+        fill_rows_without_node<__nv_bfloat16, D, RING, RS, BN>(p, warp == 10, 2, &g_status_tree_tc);
+        if (lane == 0) {
             // drain: the last copies issued must land before this CTA may exit
             for (int q = max(0, u - ST); q < u; ++q)
                 if (!wait1(&full[q % ST], (q / ST) & 1)) break;
@@ -438,8 +453,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tO = tmem + 256 + hh * 128 + lane_off;
         const uint64_t sl2 = tc::f2_pack(p.scale_log2, p.scale_log2);
         float2 *s_ml = reinterpret_cast<float2 *>(sbase + L::ML);
+        const bool o_32B = (reinterpret_cast<uintptr_t>(p.o) & 31u) == 0;
         bool ok = true;
-        int u = 0, seg = 0, g[2] = {0, 0}, k[2] = {0, 0};   // as the issuer's
+        int u = 0, seg = 0, g[2] = {0, 0}, k[2] = {0, 0};   // tiles, segments, and each chain's
         for (; ok && it.next(p, sg); ++seg) {
             const int nt = sg.t1 - sg.t0;
             const int row = sg.rt * RS + (PAIR ? hh * 128 : 0) + r;   // of the stream's KV head
@@ -468,17 +484,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int lo1 = __shfl_sync(0xffffffffu, x1.lo, src), hi1 = __shfl_sync(0xffffffffu, x1.hi, src);
                     if (live) rb = node < 32 ? RingBounds{lo0, hi0} : RingBounds{lo1, hi1};
                     if (with_nodes) {
-                        const int64_t m0 = __shfl_sync(0xffffffffu, p0, src), m1 = __shfl_sync(0xffffffffu, p1, src);
-                        const uint64_t mine = (uint64_t)(node < 32 ? m0 : m1);
+                        // node by node of the warp's rows: which nodes lie in its window, a
+                        // ballot of the lanes' two
 #pragma unroll 4
-                        for (int j = 0; j < sg.n; ++j) {
-                            const int64_t other = __shfl_sync(0xffffffffu, j < 32 ? p0 : p1, j & 31);
-                            if (mine - (uint64_t)other >= (uint64_t)p.window) vis &= ~(1ull << j);
+                        for (int i = 0; i < 32 >> p.lg; ++i) {
+                            const int at = __shfl_sync(0xffffffffu, node, i << p.lg) & 63;
+                            const int64_t m0 = __shfl_sync(0xffffffffu, p0, at & 31), m1 = __shfl_sync(0xffffffffu, p1, at & 31);
+                            const uint64_t mine = (uint64_t)(at < 32 ? m0 : m1);
+                            const uint32_t w0 = __ballot_sync(0xffffffffu, mine - (uint64_t)p0 < (uint64_t)p.window);
+                            const uint32_t w1 = __ballot_sync(0xffffffffu, mine - (uint64_t)p1 < (uint64_t)p.window);
+                            if (lane >> p.lg == i) vis &= (uint64_t)w1 << 32 | w0;
                         }
                     }
                 }
             }
             if (sg.n < 64) vis &= (1ull << sg.n) - 1;
+
+            // stored positions of this chain's next ring tile, slot 128 t + lane + 32 e in
+            // next_sp[e]: loaded a tile ahead
+            int next_sp[4] = {-1, -1, -1, -1};
+            auto load_slots = [&](int t) {
+                if (RING && t < min(sg.t1, sg.n_ctx_tiles)) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int j = t * BN + lane + 32 * e;
+                        next_sp[e] = j < sg.ctx ? p.slot_pos[sg.row0 + j] : -1;
+                    }
+                }
+            };
+            load_slots(sg.t0 + (PAIR ? 0 : hh));
 
             float m = -INFINITY, l = 0.f;
             bool first = true;
@@ -489,8 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const bool nodes = t == sg.n_ctx_tiles;
                 const int j0 = t * BN;
-                // is the tile seen whole by every row?  A ring tile's stored positions
-                // in four registers a lane, slot j0 + lane + 32 e in sp[e]
+                // is the tile seen whole by every row?
                 bool masked = nodes || j0 + BN > sg.ctx;
                 int sp[4];
                 if constexpr (RING) {
@@ -498,12 +531,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         bool all = true;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int j = j0 + lane + 32 * e;
-                            sp[e] = j < sg.ctx ? p.slot_pos[sg.row0 + j] : -1;
+                            sp[e] = next_sp[e];
                             all &= span.every.hi > span.every.lo && span.every.sees(sp[e]);
                         }
                         masked = !__all_sync(0xffffffffu, all);
                     }
+                    load_slots(t + (PAIR ? 1 : 2));
                 }
                 if (!waitw(&bars[kSFull + hh], g[hh] & 1)) { ok = false; break; }
                 tc::fence_after_sync();
@@ -514,28 +547,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int at = PAIR ? u : 2 * g[hh] + 1;   // copies before it in its ring
                     const int vst = PAIR || hh == 1 ? L::VST : L::KST, v0 = PAIR || hh == 1 ? kVFull : kKFull;
                     if (!waitw(&bars[v0 + at % vst], (at / vst) & 1)) { ok = false; break; }
-                    bool unseen, whole_row = false;
+                    uint8_t *tile = sbase + (PAIR || hh == 1 ? L::V : L::K) + (at % vst) * L::TILE;
+                    bool odd = false;
                     if (nodes) {
-                        unseen = r >= sg.n;
+                        // 64 rows, two threads a row
+                        odd = clean_v_row<KB, 4>(tile, r & 63, (r >> 6) * 4, (r & 63) >= sg.n);
                     } else if (RING) {
                         int s = -1;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) s = (warp & 3) == e ? sp[e] : s;
-                        unseen = !(span.any.hi > span.any.lo && span.any.sees(s));
-                    } else {
-                        unseen = j0 + r >= sg.ctx;
-                        whole_row = !unseen;   // every row sees it: what it holds counts for all
+                        if (!(span.every.hi > span.every.lo && span.every.sees(s)))
+                            odd = clean_v_row<KB, 8>(tile, r, 0, !(span.any.hi > span.any.lo && span.any.sees(s)));
+                    } else if (j0 + r >= sg.ctx) {
+                        clean_v_row<KB, 8>(tile, r, 0, true);
                     }
-                    if (!whole_row && !(nodes && r >= kTreeMaxNodes)) {
-                        if (clean_v_row<KB>(sbase + (PAIR || hh == 1 ? L::V : L::K) + (at % vst) * L::TILE, r, unseen))
-                            *(volatile int *)&misc->poison[seg & 7] = seg;
-                        fence_proxy_async_smem();
-                    }
-                }
-                if (PAIR && hh == 0) {
-                    // chain B's P V reads this tile too
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars[kVClean + u % L::VST]);
+                    if (odd) *(volatile int *)&misc->poison[seg & 7] = seg;
+                    fence_proxy_async_smem();
                 }
                 if (active) {
                     float s[BN];
@@ -642,7 +669,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 first = false;
                 tc::fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[kPFull + hh]);
+                if (lane == 0) {
+                    mbar_arrive(&bars[kPFull + hh]);
+                    if (PAIR && hh == 0) mbar_arrive(&bars[kVClean + u % L::VST]);   // chain B's P V reads this tile too
+                }
                 ++g[hh];
             }
             if (!ok) break;
@@ -710,14 +740,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     if (live && sg.whole) {
+                        // 32-byte stores where o allows them: a thread's row is its own, so a
+                        // warp's store covers 32 rows, and these are whole sectors
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            uint4 wv;
-                            wv.x = tc::pack_bf16x2(o[e] * inv, o[e + 1] * inv);
-                            wv.y = tc::pack_bf16x2(o[e + 2] * inv, o[e + 3] * inv);
-                            wv.z = tc::pack_bf16x2(o[e + 4] * inv, o[e + 5] * inv);
-                            wv.w = tc::pack_bf16x2(o[e + 6] * inv, o[e + 7] * inv);
-                            *reinterpret_cast<uint4 *>(dst + c + e) = wv;
+                        for (int e = 0; e < 32; e += 16) {
+                            uint32_t wv[8];
+#pragma unroll
+                            for (int u = 0; u < 8; ++u) wv[u] = tc::pack_bf16x2(o[e + 2 * u] * inv, o[e + 2 * u + 1] * inv);
+                            if (o_32B) {
+                                st_global_32B(dst + c + e, wv);
+                            } else {
+                                *reinterpret_cast<uint4 *>(dst + c + e) = make_uint4(wv[0], wv[1], wv[2], wv[3]);
+                                *reinterpret_cast<uint4 *>(dst + c + e + 8) = make_uint4(wv[4], wv[5], wv[6], wv[7]);
+                            }
                         }
                     } else if (live) {
 #pragma unroll
