@@ -359,9 +359,11 @@ yoco_status yoco_rope(const void *q, const void *k, int32_t B, int64_t T, const 
  *  - A row that sees no key, or whose node does not exist: o = 0, lse = -inf.
  *    What an unseen key's K and V hold (infinities, NaN) has no effect.
  *  - lse [B, Hq, N] or NULL.
- *  - workspace: device scratch of the size query's bytes; it needs no clearing
- *    and keeps nothing between calls, but calls whose kernels may overlap need
- *    one each.  Two launches, no host synchronisation.
+ *  - workspace: device scratch of the size query's bytes, NULL where that says 0
+ *    (few streams, none of them long: the CTAs of a cluster join their parts
+ *    themselves); it needs no clearing and keeps nothing between calls, but
+ *    calls whose kernels may overlap need one each.  The size query returns 0
+ *    on bad arguments too.  At most two launches, no host synchronisation.
  *  - A sequence whose device-side arguments are out of range (n_nodes outside
  *    [0, N], or as stated below) reads nothing; its o is 0 and its lse -inf,
  *    the others are computed, and the next yoco_get_device_status returns

@@ -603,7 +603,8 @@ def _tree_args(q, k_nodes, v_nodes, tree_mask, n_nodes, context, workspace, o, w
         _want(n_nodes, "n_nodes", _I32, (B,), device)
     if workspace is None:
         ws_bytes = _tree_ws(device, B, N, context, Hq, Hkv, D, dtype)
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+        if ws_bytes > 0:
+            workspace = q.new_empty(ws_bytes, dtype=torch.uint8)
     elif workspace.get_device() != device or not workspace.is_contiguous():
         raise ValueError(f"workspace: a contiguous tensor on cuda:{device}")
     else:
@@ -612,8 +613,8 @@ def _tree_args(q, k_nodes, v_nodes, tree_mask, n_nodes, context, workspace, o, w
         o = torch.empty_like(q)
     else:
         _want(o, "o", dtype, shape, device)
-    lse = torch.empty((B, Hq, N), dtype=torch.float32, device=q.device) if want_lse else None
-    return B, N, Hq, Hkv, D, device, workspace.data_ptr(), ws_bytes, o, lse, workspace
+    lse = q.new_empty((B, Hq, N), dtype=torch.float32) if want_lse else None
+    return B, N, Hq, Hkv, D, device, _addr(workspace), ws_bytes, o, lse, workspace
 
 
 def cross_decode_tree(q, k_nodes, v_nodes, k_cache, v_cache, seq_start, seq_len, max_len, tree_mask=None,

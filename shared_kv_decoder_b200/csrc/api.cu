@@ -481,7 +481,7 @@ yoco_status yoco_cross_decode_tree(const void *q, const void *k_nodes, const voi
         return YOCO_ERR_INVALID;
     TreePlan pl;
     if (!make_tree_plan(B, N, max_len, cfg->Hq, cfg->Hkv, cfg->D, cfg->dtype, &pl)) return YOCO_ERR_UNSUPPORTED;
-    if (!ok_ptr(workspace) || ws_bytes < pl.ws_bytes) return YOCO_ERR_WORKSPACE;
+    if (pl.ws_bytes > 0 && (!ok_ptr(workspace) || ws_bytes < pl.ws_bytes)) return YOCO_ERR_WORKSPACE;
     TreeArgs a;
     a.q = q; a.k_nodes = k_nodes; a.v_nodes = v_nodes; a.k = k_cache; a.v = v_cache;
     a.seq_start = seq_start; a.seq_len = seq_len; a.slot_pos = nullptr; a.node_pos = nullptr;
@@ -507,7 +507,7 @@ yoco_status yoco_swa_decode_tree(const void *q, const void *k_nodes, const void 
         return YOCO_ERR_INVALID;
     TreePlan pl;
     if (!make_tree_plan(B, N, window, cfg->Hq, cfg->Hkv, cfg->D, cfg->dtype, &pl)) return YOCO_ERR_UNSUPPORTED;
-    if (!ok_ptr(workspace) || ws_bytes < pl.ws_bytes) return YOCO_ERR_WORKSPACE;
+    if (pl.ws_bytes > 0 && (!ok_ptr(workspace) || ws_bytes < pl.ws_bytes)) return YOCO_ERR_WORKSPACE;
     TreeArgs a;
     a.q = q; a.k_nodes = k_nodes; a.v_nodes = v_nodes; a.k = ring_k; a.v = ring_v;
     a.seq_start = nullptr; a.seq_len = nullptr; a.slot_pos = slot_pos; a.node_pos = node_pos;

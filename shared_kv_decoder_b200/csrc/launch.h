@@ -149,7 +149,8 @@ constexpr int kTreeMaxNodes = 64;
 
 struct TreePlan {
     int rows, keys;           // rows of a stream, keys of a tile (tree.cuh)
-    int heads, groups;        // CTAs: groups of `heads`
+    int cluster;              // CTAs that share a stream in a cluster; 0: the numbered shares
+    int heads, groups;        // of them: CTAs, groups of `heads`
     size_t ml_off, o_off, ws_bytes;
 };
 // max_len: the longest context (a ring: its window).

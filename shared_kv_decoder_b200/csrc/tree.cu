@@ -27,6 +27,11 @@ constexpr int kSimtRows = 32;     // RS of the CUDA-core kernel
 constexpr int kSimtKeys = 64;     // BN of the CUDA-core kernel
 constexpr int kMergeWarps = 8;
 constexpr int kGroupHeads = 8;
+#ifndef TREE_MAX_CLUSTER
+#define TREE_MAX_CLUSTER 8
+#endif
+constexpr int kMaxCluster = TREE_MAX_CLUSTER;
+constexpr int kClusterTiles = 16;    // tiles of a CTA of a cluster at most
 constexpr int64_t kFewRows = 4096;   // rows that four merge warps each still serve in about a wave
 
 template <typename T>
@@ -384,7 +389,7 @@ template <int D, bool RING>
 cudaError_t launch_d(const TreeArgs &a, const TreePlan &pl, cudaStream_t st) {
     if (a.dtype == kBF16) {
         const cudaError_t e = launch_tree_tc(a, pl, st);
-        if (e != cudaSuccess) return e;
+        if (e != cudaSuccess || pl.cluster) return e;
         return pl.rows == 128 ? launch_merge<__nv_bfloat16, D, RING, 128, kTcKeys>(a, pl, st)
                               : launch_merge<__nv_bfloat16, D, RING, 256, kTcKeys>(a, pl, st);
     }
@@ -401,13 +406,27 @@ bool make_tree_plan(int32_t B, int32_t N, int64_t max_len, int Hq, int Hkv, int 
     // bf16: the tensor-core kernel, one row tile of 128 or two; fp32: CUDA cores
     pl.rows = dtype != kBF16 ? tree::kSimtRows : N * (Hq / Hkv) <= 128 ? 128 : 256;
     pl.keys = dtype != kBF16 ? tree::kSimtKeys : tree::kTcKeys;
+    const int n_rt = (N * (Hq / Hkv) + pl.rows - 1) / pl.rows;
+    const int64_t stream_tiles = (max_len + pl.keys - 1) / pl.keys + 1;
+    // bf16, few streams, none of them long: a cluster a stream, no second launch
+    // and no numbering to work out first
+    pl.cluster = 0;
+    if (dtype == kBF16 && max_len <= INT32_MAX / 2)
+        for (int c = 2; c <= tree::kMaxCluster; c *= 2)
+            if ((int64_t)B * n_rt * Hkv * c <= device_sm_count() && stream_tiles <= (int64_t)c * tree::kClusterTiles) pl.cluster = c;
+    if (pl.cluster) {
+        pl.heads = pl.groups = 1;
+        pl.ml_off = pl.o_off = pl.ws_bytes = 0;
+        *plan = pl;
+        return true;
+    }
     // groups of CTAs, one KV head of a block each (tree.cuh): the largest divisor of Hkv up to 8
     pl.heads = 1;
     for (int h = 2; h <= tree::kGroupHeads; ++h)
         if (Hkv % h == 0) pl.heads = h;
     // tiles at full length: no group without a tile is launched
-    const int64_t blocks = (int64_t)B * ((N * (Hq / Hkv) + pl.rows - 1) / pl.rows) * (Hkv / pl.heads);
-    const int64_t tiles = blocks * ((max_len + pl.keys - 1) / pl.keys + 1);
+    const int64_t blocks = (int64_t)B * n_rt * (Hkv / pl.heads);
+    const int64_t tiles = blocks * stream_tiles;
     if ((int64_t)B * N * Hq > (int64_t)INT32_MAX / 2 || tiles > INT32_MAX / 2) return false;
     const int64_t ctas = (int64_t)(dtype != kBF16 ? 2 : 1) * device_sm_count();
     pl.groups = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, ctas / pl.heads));

@@ -45,6 +45,7 @@ struct Params {
     int32_t B, N, Hq, Hkv;
     int32_t lg;                          // log2 of Hq / Hkv
     int32_t heads, groups;               // KV heads of a CTA group; groups
+    int32_t cluster;                     // CTAs of a cluster, 0: no clusters
     int32_t window;                      // 0: cache
     int64_t cache_rows, max_len;
     float scale_log2;
@@ -226,6 +227,43 @@ struct SegIter {
     }
 };
 
+// The one segment of a CTA of a cluster: cluster c has stream c (sequence by
+// sequence, row blocks outermost, at their full number), and its CTAs an equal
+// share of the stream's tiles each.
+struct ClusterIter {
+    Seg s;
+    bool any;
+    YOCO_DEV bool next(const Params &, Seg &g) {
+        if (!any) return false;
+        any = false;
+        g = s;
+        return true;
+    }
+};
+
+template <bool RING, int RS, int BN>
+YOCO_DEV ClusterIter cluster_share(const Params &p, int cluster, int rank, int size, Seq *seq) {
+    ClusterIter it;
+    const int n_rt = ((p.N << p.lg) + RS - 1) / RS, per_b = n_rt * p.Hkv;
+    it.s.b = cluster / per_b;
+    const int stream = cluster - it.s.b * per_b;
+    it.s.rt = stream / p.Hkv;
+    it.s.g = stream - it.s.rt * p.Hkv;
+    const Seq q = sequence<RING, RS, BN>(p, it.s.b);
+    const int nt = it.s.rt < q.n_rt ? q.n_ctx_tiles + 1 : 0;
+    it.s.n = q.n;
+    it.s.n_ctx_tiles = q.n_ctx_tiles;
+    it.s.ctx = q.ctx;
+    it.s.row0 = q.row0;
+    it.s.t0 = (int)((unsigned)(rank * nt) / (unsigned)size);
+    it.s.t1 = (int)((unsigned)((rank + 1) * nt) / (unsigned)size);
+    it.s.whole = false;
+    it.s.slot = 0;
+    it.any = it.s.t0 < it.s.t1;
+    *seq = q;
+    return it;
+}
+
 // Rows without a node, and every row of a sequence out of range (which is
 // reported as bit 1 of *status): o = 0, lse = -inf.  Warp w of `warps` of every
 // CTA takes its share of the (sequence, node) pairs.
@@ -282,7 +320,7 @@ inline Params make_params(const TreeArgs &a, const TreePlan &pl) {
     p.mask = a.mask; p.n_nodes = a.n_nodes;
     p.B = a.B; p.N = a.N; p.Hq = a.Hq; p.Hkv = a.Hkv; p.window = a.window;
     p.lg = a.Hq / a.Hkv == 8 ? 3 : a.Hq / a.Hkv == 4 ? 2 : a.Hq / a.Hkv == 2 ? 1 : 0;
-    p.heads = pl.heads; p.groups = pl.groups;
+    p.heads = pl.heads; p.groups = pl.groups; p.cluster = pl.cluster;
     p.cache_rows = a.cache_rows; p.max_len = a.max_len;
     p.scale_log2 = a.scale * kLog2e;
     p.o = a.o; p.lse = a.lse;

@@ -43,7 +43,9 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
+#include "cluster.cuh"
 #include "common.cuh"
 #include "launch.h"
 #include "tc.cuh"
@@ -76,7 +78,7 @@ struct Smem {
     static constexpr uint32_t ML = V + VST * TILE;      // float2[128]: chain B's (m, l)
     static constexpr uint32_t BAR = ML + 128 * 8;
     static constexpr uint32_t MISC = BAR + 48 * 8;
-    static constexpr uint32_t BYTES = MISC + 192;
+    static constexpr uint32_t BYTES = MISC + 256;
     static constexpr uint32_t ALLOC = BYTES + 1024;     // alignment slack
 };
 static_assert(Smem<128, true>::ALLOC <= 232448 && Smem<128, false>::ALLOC <= 232448, "shared memory");
@@ -102,10 +104,12 @@ enum Bar {
 struct Misc {
     uint32_t tmem;
     int abort;
+    ClusterIter share;
+    Seq seq;
     int poison[8];   // by segment mod 8: the last segment with an infinity or NaN cleared from a seen V row
     Range range;
 };
-static_assert(sizeof(Misc) <= 192, "misc area");
+static_assert(sizeof(Misc) <= 256, "misc area");
 
 YOCO_DEV bool wait1(uint64_t *bar, uint32_t parity) { return mbar_wait(bar, parity, &g_status_tree_tc); }
 YOCO_DEV bool waitw(uint64_t *bar, uint32_t parity) {
@@ -131,12 +135,12 @@ YOCO_DEV bool clean_v_row(uint8_t *tile, int r, int c0, bool unseen) {
         return reinterpret_cast<uint4 *>(row + i / NC * kBlk + (((c0 + i % NC) ^ (r & 7)) << 4));
     };
     if (unseen) {
-#pragma unroll
+#pragma unroll 4
         for (int i = 0; i < NC * KB; ++i) *at(i) = make_uint4(0, 0, 0, 0);
         return false;
     }
     uint32_t odd = 0;
-#pragma unroll
+#pragma unroll 4
     for (int i = 0; i < NC * KB; ++i) {
         const uint4 v = *at(i);
         odd |= odd_bits(v.x) | odd_bits(v.y) | odd_bits(v.z) | odd_bits(v.w);
@@ -218,7 +222,7 @@ struct RingSpan {
 
 }  // namespace
 
-template <int D, bool RING, bool PAIR>
+template <int D, bool RING, bool PAIR, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kn,
@@ -226,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     using L = Smem<D, PAIR>;
     constexpr int KB = L::KB;
     constexpr int RS = PAIR ? 256 : 128;
-    using Iter = SegIter<RING, RS, BN>;
+    using Iter = std::conditional_t<CLUSTER, ClusterIter, SegIter<RING, RS, BN>>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -273,15 +277,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     pdl_wait();
     if (warp == 8) {
-        find_range<RING, RS, BN>(p, &misc->range);
         // once any CTA has recorded a timeout, the rest of the grid does nothing
-        if (lane == 0 && *(volatile unsigned int *)&g_status_tree_tc & 1u) misc->range.x = misc->range.end;
+        const bool idle = *(volatile unsigned int *)&g_status_tree_tc & 1u;
+        if constexpr (CLUSTER) {
+            if (lane == 0) {
+                Seq q;
+                ClusterIter s = cluster_share<RING, RS, BN>(p, (int)blockIdx.x / p.cluster, (int)blockIdx.x % p.cluster,
+                                                            p.cluster, &q);
+                if (idle) s.any = false;
+                misc->share = s;
+                misc->seq = q;
+                if (!q.ok && s.s.g == 0 && s.s.rt == 0) atomicOr(&g_status_tree_tc, kStatusBadSequence);
+            }
+        } else {
+            find_range<RING, RS, BN>(p, &misc->range);
+            if (lane == 0 && idle) misc->range.x = misc->range.end;
+        }
     }
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = misc->tmem;
-    Iter it(p, misc->range);
+    Iter it = [&] {
+        if constexpr (CLUSTER) return misc->share;
+        else return Iter(p, misc->range);
+    }();
     Seg sg;
 
     if (warp == 8 || warp == 10) {
@@ -329,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         // with every copy issued, these warps have time
-        fill_rows_without_node<__nv_bfloat16, D, RING, RS, BN>(p, warp == 10, 2, &g_status_tree_tc);
+        if (!CLUSTER) fill_rows_without_node<__nv_bfloat16, D, RING, RS, BN>(p, warp == 10, 2, &g_status_tree_tc);
         if (lane == 0) {
             // drain: the last copies issued must land before this CTA may exit
             for (int q = max(0, u - ST); q < u; ++q)
@@ -348,7 +368,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // leading offset, so a step is one 32-bit addition
             constexpr uint32_t kHi = (1024u >> 4) | 1u << 14 | 2u << 29;
             constexpr uint32_t kLoS = (16u >> 4) << 16, kLoV = (kBlk >> 4) << 16;
-            const uint32_t q_lo = ((base + L::Q + (PAIR ? hh * L::TILE : 0)) >> 4) | kLoS;
+            // (a CTA of a cluster has its rank in the bits above its shared-memory offsets)
+            const uint32_t off0 = base & 0x3ffffu;
+            const uint32_t q_lo = ((off0 + L::Q + (PAIR ? hh * L::TILE : 0)) >> 4) | kLoS;
             const uint32_t ts = tmem + hh * 128, to = tmem + 256 + hh * 128;
             auto desc = [](uint32_t lo) { return (uint64_t)kHi << 32 | lo; };
             uint64_t *q_full = &bars[kQFull + (PAIR ? hh : 0)], *q_empty = &bars[kQEmpty + (PAIR ? hh : 0)];
@@ -366,9 +388,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             };
             const bool one = PAIR || hh == 0;
-            Ring rk = {&bars[one ? kKFull : kVFull], &bars[one ? kKEmpty : kVEmpty], (base + (one ? L::K : L::V)) >> 4, 0,
+            Ring rk = {&bars[one ? kKFull : kVFull], &bars[one ? kKEmpty : kVEmpty], (off0 + (one ? L::K : L::V)) >> 4, 0,
                        0, L::KST};
-            Ring rv_own = {&bars[kVFull], &bars[kVEmpty], (base + L::V) >> 4, 0, 0, L::VST};
+            Ring rv_own = {&bars[kVFull], &bars[kVEmpty], (off0 + L::V) >> 4, 0, 0, L::VST};
             Ring &rv = PAIR ? rv_own : rk;
             bool ok = true;
             int seg = 0;
@@ -462,6 +484,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int node = row >> p.lg;
             const bool live = node < sg.n;
             const bool active = __any_sync(0xffffffffu, live);        // some row of the warp
+            // stored positions of this chain's next ring tile, slot 128 t + lane + 32 e in
+            // next_sp[e]: loaded a tile ahead
+            int next_sp[4] = {-1, -1, -1, -1};
+            auto load_slots = [&](int t) {
+                if (RING && t < min(sg.t1, sg.n_ctx_tiles)) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int j = t * BN + lane + 32 * e;
+                        next_sp[e] = j < sg.ctx ? p.slot_pos[sg.row0 + j] : -1;
+                    }
+                }
+            };
+            load_slots(sg.t0 + (PAIR ? 0 : hh));
+
             // what this row sees; the nodes only matter to the segment with their tile
             const bool with_nodes = sg.t1 > sg.n_ctx_tiles;
             uint64_t vis = 0;
@@ -499,20 +535,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (sg.n < 64) vis &= (1ull << sg.n) - 1;
-
-            // stored positions of this chain's next ring tile, slot 128 t + lane + 32 e in
-            // next_sp[e]: loaded a tile ahead
-            int next_sp[4] = {-1, -1, -1, -1};
-            auto load_slots = [&](int t) {
-                if (RING && t < min(sg.t1, sg.n_ctx_tiles)) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int j = t * BN + lane + 32 * e;
-                        next_sp[e] = j < sg.ctx ? p.slot_pos[sg.row0 + j] : -1;
-                    }
-                }
-            };
-            load_slots(sg.t0 + (PAIR ? 0 : hh));
 
             float m = -INFINITY, l = 0.f;
             bool first = true;
@@ -595,8 +617,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 w[e] = x >= 32 ? 0xffffffffu : x <= 0 ? 0u : (1u << x) - 1u;
                             }
                         }
+                        // most masked tiles are masked in one chunk of 32 columns
 #pragma unroll
-                        for (int c = 0; c < BN; ++c) s[c] = (w[c >> 5] >> (c & 31)) & 1u ? s[c] : -INFINITY;
+                        for (int e = 0; e < 4; ++e)
+                            if (!__all_sync(0xffffffffu, w[e] == 0xffffffffu)) {
+#pragma unroll
+                                for (int c = 0; c < 32; ++c) s[32 * e + c] = w[e] >> c & 1u ? s[32 * e + c] : -INFINITY;
+                            }
                     }
                     float a8[8];
 #pragma unroll
@@ -690,6 +717,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 continue;
             }
             if (!waitw(&bars[kODone + hh], (g[hh] - 1) & 1)) { ok = false; break; }
+            // the partial goes over the tiles in shared memory: nobody reads them any more
+            if (CLUSTER && PAIR && !waitw(&bars[kODone + (hh ^ 1)], (g[hh] - 1) & 1)) { ok = false; break; }
             float wa = 1.f, wb = 0.f;
             const bool join = !PAIR && has_b;
             if (join) {
@@ -739,7 +768,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                 ((sg.row0 + j) * p.Hkv + sg.g) * D + c, o);
                         }
                     }
-                    if (live && sg.whole) {
+                    if (CLUSTER) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4 *>(sbase + ((uint32_t)ws_row * (D + 4) + c + e) * 4) =
+                                make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    } else if (live && sg.whole) {
                         // 32-byte stores where o allows them: a thread's row is its own, so a
                         // warp's store covers 32 rows, and these are whole sectors
 #pragma unroll
@@ -769,12 +803,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(&bars[kOFree + hh]);
                 if (join) mbar_arrive(&bars[kOFree + 1]);
             }
-            if (live && sg.whole && p.lse)
+            if (CLUSTER) reinterpret_cast<float2 *>(sbase + RS * (D + 4) * 4)[ws_row] = make_float2(m, l);
+            if (!CLUSTER && live && sg.whole && p.lse)
                 p.lse[((int64_t)sg.b * p.Hq + head) * p.N + node] = none ? -INFINITY : (m + __log2f(l)) * kLn2;
-            if (live && !sg.whole) p.ws_ml[entry * RS + ws_row] = make_float2(m, l);
+            if (!CLUSTER && live && !sg.whole) p.ws_ml[entry * RS + ws_row] = make_float2(m, l);
             ++k[0];
             k[1] += has_b;
         }
+        // a CTA without a tile, and one that gave up: nothing to add
+        if (CLUSTER && (seg == 0 || !ok) && (PAIR || hh == 0))
+            reinterpret_cast<float2 *>(sbase + RS * (D + 4) * 4)[(PAIR ? hh * 128 : 0) + r] = make_float2(-INFINITY, 0.f);
         if (!ok) *abort_flag = 1;
         tc::wait_st();   // no TMEM store may be in flight when TMEM is freed
     }
@@ -784,6 +822,55 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 9) {
         tc::fence_after_sync();
         tc::tmem_dealloc(tmem, kTmemCols);
+    }
+    if constexpr (CLUSTER) {
+        // Join the partials of the cluster's CTAs: every warp of every CTA has rows of
+        // its own, and reads them from all of them.  Rows without a node come out as
+        // zeros.  Every CTA gets here whatever happened before: its waits are bounded.
+        __syncwarp();
+        clu::sync_all();
+        const Seg &s = misc->share.s;
+        const int P = p.cluster, rank = (int)clu::rank();
+        const int rows = min(RS, (p.N << p.lg) - s.rt * RS);
+        const uint32_t ml0 = base + RS * (D + 4) * 4;
+        for (int i = warp * P + rank; i < rows; i += P * (kThreads / 32)) {
+            const int row = s.rt * RS + i, node = row >> p.lg, head = (s.g << p.lg) + (row & ((1 << p.lg) - 1));
+            float m = -INFINITY, l = 0.f;
+            if (node < s.n && lane < P) {
+                const uint32_t at = clu::map_rank(ml0 + i * 8, lane);
+                asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(m), "=f"(l) : "r"(at) : "memory");
+            }
+            const bool some = !(m == -INFINITY && l == 0.f);
+            const uint32_t parts = __ballot_sync(0xffffffffu, some);
+            const float mm = warp_max(m), ref = mm == -INFINITY ? 0.f : mm;
+            const float w = some ? tc::ex2(m - ref) : 0.f;
+            const float sum = warp_sum(w * l);
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int j = 0; j < P; ++j) {
+                const float wj = __shfl_sync(0xffffffffu, w, j);
+                if (!((parts >> j) & 1) || lane >= D / 4) continue;
+                float4 o;
+                asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                             : "=f"(o.x), "=f"(o.y), "=f"(o.z), "=f"(o.w)
+                             : "r"(clu::map_rank(base + ((uint32_t)i * (D + 4) + 4 * lane) * 4, j))
+                             : "memory");
+                acc.x = fmaf(wj, o.x, acc.x);
+                acc.y = fmaf(wj, o.y, acc.y);
+                acc.z = fmaf(wj, o.z, acc.z);
+                acc.w = fmaf(wj, o.w, acc.w);
+            }
+            const float inv = parts ? 1.f / sum : 0.f;
+            if (lane < D / 4) {
+                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.o) + (((int64_t)s.b * p.N + node) * p.Hq + head) * D;
+                *reinterpret_cast<uint2 *>(dst + 4 * lane) =
+                    make_uint2(tc::pack_bf16x2(acc.x * inv, acc.y * inv), tc::pack_bf16x2(acc.z * inv, acc.w * inv));
+            }
+            if (p.lse && lane == 0)
+                p.lse[((int64_t)s.b * p.Hq + head) * p.N + node] = parts ? (mm + __log2f(sum)) * kLn2 : -INFINITY;
+        }
+        __syncwarp();
+        clu::sync_all();   // no CTA leaves while another reads its shared memory
     }
 }
 
@@ -810,12 +897,31 @@ cudaError_t launch_tc(const TreeArgs &a, const TreePlan &pl, cudaStream_t st) {
         !make_map(&mkn, a.k_nodes, D, a.Hkv, a.N, a.B, 1, kTreeMaxNodes) ||
         !make_map(&mvn, a.v_nodes, D, a.Hkv, a.N, a.B, 1, kTreeMaxNodes))
         return cudaErrorNotSupported;
-    auto kern = tree_tc_kernel<D, RING, PAIR>;
     constexpr size_t smem = Smem<D, PAIR>::ALLOC;
+    const bool cl = pl.cluster > 0;
+    auto kern = cl ? tree_tc_kernel<D, RING, PAIR, true> : tree_tc_kernel<D, RING, PAIR, false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     note_launches(1);
-    return launch_pdl(kern, dim3(pl.heads * pl.groups), dim3(kThreads), smem, st, mq, mk, mv, mkn, mvn, make_params(a, pl));
+    if (!cl)
+        return launch_pdl(kern, dim3(pl.heads * pl.groups), dim3(kThreads), smem, st, mq, mk, mv, mkn, mvn,
+                          make_params(a, pl));
+    const int n_rt = (a.N * G + pl.rows - 1) / pl.rows;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.B * n_rt * a.Hkv * pl.cluster));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)pl.cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, mkn, mvn, make_params(a, pl));
 }
 
 template <int D>

@@ -54,18 +54,19 @@ SHAPES = [(4, 2, 64), (8, 8, 64), (8, 2, 128), (8, 1, 128), (4, 4, 128)]
 
 
 @pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("most", [1024, 1 << 20])    # bf16: clusters of CTAs where they fit; shares and the join
 @pytest.mark.parametrize("Hq,Hkv,D", SHAPES)
 @pytest.mark.parametrize("N,lens", [(1, [0, 1, 2, 63, 64, 65]), (3, [127, 128, 129]), (17, [300, 0, 1]),
                                     (40, [255]), (64, [1, 700])])
-def test_cross_tree(cuda_lib, dtype, Hq, Hkv, D, N, lens):
+def test_cross_tree(cuda_lib, dtype, most, Hq, Hkv, D, N, lens):
     q, kn, vn, kc, vc, starts = cross_case(dtype, lens, N, Hq, Hkv, D, 100)
     rng = np.random.default_rng(N)
     masks = [tr.random_tree(rng, N)[0] for _ in lens]
     n_nodes = [N] + [int(rng.integers(0, N + 1)) for _ in lens[1:]]
     ref = tr.cross_tree(q, kn, vn, kc, vc, starts, lens, masks, n_nodes)
-    tr.assert_tree(*run_cross(cuda_lib, q, kn, vn, kc, vc, starts, lens, masks, n_nodes), ref, dtype, "tree")
+    tr.assert_tree(*run_cross(cuda_lib, q, kn, vn, kc, vc, starts, lens, masks, n_nodes, most), ref, dtype, "tree")
     ref = tr.cross_tree(q, kn, vn, kc, vc, starts, lens, scale=0.3)
-    tr.assert_tree(*run_cross(cuda_lib, q, kn, vn, kc, vc, starts, lens, scale=0.3), ref, dtype, "chain")
+    tr.assert_tree(*run_cross(cuda_lib, q, kn, vn, kc, vc, starts, lens, max_len=most, scale=0.3), ref, dtype, "chain")
 
 
 @pytest.mark.parametrize("dtype", [BF, FP])
@@ -96,20 +97,22 @@ def test_cross_tree_many_tiles_a_segment(cuda_lib, N, Hq, Hkv, D, lens):
 
 
 @pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("most", [128, 1 << 20])
 @pytest.mark.parametrize("N,Hq,Hkv,D", [(6, 4, 2, 64), (64, 8, 2, 128)])
-def test_rows_that_see_nothing(cuda_lib, dtype, N, Hq, Hkv, D):
+def test_rows_that_see_nothing(cuda_lib, dtype, most, N, Hq, Hkv, D):
     lens = [0, 0, 5]
     q, kn, vn, kc, vc, starts = cross_case(dtype, lens, N, Hq, Hkv, D, 400)
     masks = [[0] * N, [(1 << i) if i % 3 else 0 for i in range(N)], [0] * N]
     ref = tr.cross_tree(q, kn, vn, kc, vc, starts, lens, masks)
     assert np.isneginf(ref[1][0]).all()
-    tr.assert_tree(*run_cross(cuda_lib, q, kn, vn, kc, vc, starts, lens, masks), ref, dtype)
+    tr.assert_tree(*run_cross(cuda_lib, q, kn, vn, kc, vc, starts, lens, masks, max_len=most), ref, dtype)
 
 
 @pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("most", [256, 1 << 20])
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
 @pytest.mark.parametrize("N,Hq,Hkv,D", [(5, 4, 2, 64), (40, 8, 2, 128)])
-def test_unseen_nodes_may_hold_anything_and_seen_ones_count(cuda_lib, dtype, bad, N, Hq, Hkv, D):
+def test_unseen_nodes_may_hold_anything_and_seen_ones_count(cuda_lib, dtype, most, bad, N, Hq, Hkv, D):
     lens = [130, 64]
     q, kn, vn, kc, vc, starts = cross_case(dtype, lens, N, Hq, Hkv, D, 500)
     # node 2's K and V are bad; only node 4 sees it, whose rows have to show it
@@ -118,7 +121,7 @@ def test_unseen_nodes_may_hold_anything_and_seen_ones_count(cuda_lib, dtype, bad
     kn[0, 2], vn[0, 2] = bad, bad
     vn[1, 2, :, 7] = bad                       # one element of V, seen by node 3 of sequence 1
     masks[1][3] |= 1 << 2
-    o, lse = run_cross(cuda_lib, q, kn, vn, kc, vc, starts, lens, masks)
+    o, lse = run_cross(cuda_lib, q, kn, vn, kc, vc, starts, lens, masks, max_len=most)
     go = tr.f64(o)
     assert not np.isfinite(go[0, 4]).any()
     assert not np.isfinite(go[1, 3, :, 7]).any()
@@ -148,11 +151,12 @@ def test_unseen_nodes_may_hold_anything_and_seen_ones_count(cuda_lib, dtype, bad
 
 
 @pytest.mark.parametrize("dtype", [BF, FP])
-def test_nan_in_q_stays_in_its_row(cuda_lib, dtype):
+@pytest.mark.parametrize("most", [128, 1 << 20])
+def test_nan_in_q_stays_in_its_row(cuda_lib, dtype, most):
     lens, N = [70], 4
     q, kn, vn, kc, vc, starts = cross_case(dtype, lens, N, 4, 2, 64, 550)
     q[0, 1, 2, 3] = math.nan
-    o, lse = run_cross(cuda_lib, q, kn, vn, kc, vc, starts, lens)
+    o, lse = run_cross(cuda_lib, q, kn, vn, kc, vc, starts, lens, max_len=most)
     go, gl = tr.f64(o), tr.f64(lse)
     assert np.isnan(go[0, 1, 2]).all() and np.isnan(gl[0, 2, 1])
     go[0, 1, 2], gl[0, 2, 1] = 0, 0
@@ -160,7 +164,8 @@ def test_nan_in_q_stays_in_its_row(cuda_lib, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, FP])
-def test_sequences_out_of_range(cuda_lib, dtype):
+@pytest.mark.parametrize("many", [1, 40])            # bf16: in clusters, and dealt in shares
+def test_sequences_out_of_range(cuda_lib, dtype, many):
     lens, N = [40, 33, 20, 64, 10, 12], 3
     q, kn, vn, kc, vc, starts = cross_case(dtype, lens, N, 4, 2, 64, 600)
     given, at, nodes = list(lens), list(starts), [N] * 6
@@ -169,10 +174,13 @@ def test_sequences_out_of_range(cuda_lib, dtype):
     at[3] = kc.shape[0] - 63      # runs past the cache
     nodes[4] = N + 1
     at[5] = -1
-    o, lse = run_cross(cuda_lib, q, kn, vn, kc, vc, at, given, None, nodes, max_len=64)
+    rep = lambda t: t.repeat(many, 1, 1, 1)
+    o, lse = run_cross(cuda_lib, rep(q), rep(kn), rep(vn), kc, vc, at * many, given * many, None, nodes * many, max_len=64)
     assert cuda_lib.device_status() == cuda_lib.ERR_INVALID
+    # (copies are not equal to the bit: shares cut each one's tiles elsewhere)
     ref = tr.cross_tree(q, kn, vn, kc, vc, starts, lens, None, [N, 0, 0, 0, 0, 0])
-    tr.assert_tree(o, lse, ref, dtype)
+    for i in range(0, 6 * many, 6):
+        tr.assert_tree(o[i:i + 6], lse[i:i + 6], ref, dtype)
 
 
 def ring_case(dtype, B, N, W, filled, Hq, Hkv, D, seed, empty=math.nan):
@@ -212,6 +220,21 @@ def test_swa_tree(cuda_lib, dtype, Hq, Hkv, D, W, N, filled):
     pos = [[f + i for i in range(N)] for f in filled]   # a chain, longer than the window where N > W
     ref = tr.swa_tree(q, kn, vn, pos, rk, rv, sp, W)
     tr.assert_tree(*run_swa(cuda_lib, q, kn, vn, pos, rk, rv, sp, W), ref, dtype, "chain")
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("N,Hq,Hkv,D", [(5, 8, 2, 128), (40, 16, 4, 64)])
+def test_swa_tree_many_sequences(cuda_lib, dtype, N, Hq, Hkv, D):
+    """More streams than SMs: shares that start and end anywhere."""
+    B, W = 45, 300
+    rng = np.random.default_rng(9)
+    filled = [int(x) for x in rng.integers(0, 2 * W, B)]
+    q, kn, vn, rk, rv, sp = ring_case(dtype, B, N, W, filled, Hq, Hkv, D, 750)
+    trees = [tr.random_tree(rng, N) for _ in filled]
+    masks, pos = [t[0] for t in trees], [[f + d for d in t[1]] for f, t in zip(filled, trees)]
+    n_nodes = [int(x) for x in rng.integers(0, N + 1, B)]
+    ref = tr.swa_tree(q, kn, vn, pos, rk, rv, sp, W, masks, n_nodes)
+    tr.assert_tree(*run_swa(cuda_lib, q, kn, vn, pos, rk, rv, sp, W, masks, n_nodes), ref, dtype)
 
 
 @pytest.mark.parametrize("dtype", [BF, FP])
@@ -407,7 +430,8 @@ def test_drafting_step_by_step(cuda_lib, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, FP])
-def test_graph_replay_and_two_streams(cuda_lib, dtype):
+@pytest.mark.parametrize("most", [512, 1 << 20])     # with clusters (bf16), with a workspace
+def test_graph_replay_and_two_streams(cuda_lib, dtype, most):
     """Captured once, replayed on new inputs; and two calls at once on two streams,
     each with its own workspace."""
     lens, N, Hq, Hkv, D = [500, 64, 0], 9, 8, 2, 128
@@ -419,10 +443,11 @@ def test_graph_replay_and_two_streams(cuda_lib, dtype):
     dev = [[t.cuda() for t in c[:5]] + [tr.mask_tensor(m, N).cuda()] for c, m in zip(cases, masks)]
     live = [t.clone() for t in dev[0]]
     ss, sl = i64(starts), i32(lens)
-    n = cuda_lib.cross_decode_tree_workspace_size(len(lens), N, 512, Hq, Hkv, D, dtype)
+    n = cuda_lib.cross_decode_tree_workspace_size(len(lens), N, most, Hq, Hkv, D, dtype)
+    assert (n == 0) == (dtype == BF and most == 512)
 
     def call(x, ws):
-        return cuda_lib.cross_decode_tree(*x[:5], ss, sl, 512, tree_mask=x[5], want_lse=True, workspace=ws)
+        return cuda_lib.cross_decode_tree(*x[:5], ss, sl, most, tree_mask=x[5], want_lse=True, workspace=ws)
     ws = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for _ in range(2)]
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
@@ -481,7 +506,8 @@ def test_python_refusals(cuda_lib):
         with pytest.raises(ValueError):
             cuda_lib.cross_decode_tree(**{**good, name: bad})
     with pytest.raises(cuda_lib.YocoError):
-        cuda_lib.cross_decode_tree(**good, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        cuda_lib.cross_decode_tree(**{**good, "max_len": 1 << 20},
+                                   workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError):
         cuda_lib.cross_tree_commit(kn, vn, i64([[0, 1]]), i32([1]), kc, vc, i64(starts), i32([8]))
     sl = i32([8])
