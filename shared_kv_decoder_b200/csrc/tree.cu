@@ -27,10 +27,6 @@ constexpr int kSimtRows = 32;     // RS of the CUDA-core kernel
 constexpr int kSimtKeys = 64;     // BN of the CUDA-core kernel
 constexpr int kMergeWarps = 8;
 constexpr int kGroupHeads = 8;
-#ifndef TREE_MAX_CLUSTER
-#define TREE_MAX_CLUSTER 8
-#endif
-constexpr int kMaxCluster = TREE_MAX_CLUSTER;
 constexpr int kClusterTiles = 16;    // tiles of a CTA of a cluster at most
 constexpr int64_t kFewRows = 4096;   // rows that four merge warps each still serve in about a wave
 
@@ -409,11 +405,17 @@ bool make_tree_plan(int32_t B, int32_t N, int64_t max_len, int Hq, int Hkv, int 
     const int n_rt = (N * (Hq / Hkv) + pl.rows - 1) / pl.rows;
     const int64_t stream_tiles = (max_len + pl.keys - 1) / pl.keys + 1;
     // bf16, few streams, none of them long: a cluster a stream, no second launch
-    // and no numbering to work out first
+    // and no numbering to work out first (16 nodes over 1 x 2047 tokens 12.3 us,
+    // as shares 19.3; over 8 x 3900 28.0 and 38.5; over 1 x 15000 25.4 and 26.5).
+    // All clusters have to run at once -- 16 clusters of eight took two rounds
+    // and lost to the shares -- and the GPU's partitions hold 15 of eight CTAs this
+    // big, 33 of four and 74 of two.
+    const int sms = device_sm_count(), room[3] = {sms / 2, (sms - 16) / 4, (sms - 28) / 8};
     pl.cluster = 0;
-    if (dtype == kBF16 && max_len <= INT32_MAX / 2)
-        for (int c = 2; c <= tree::kMaxCluster; c *= 2)
-            if ((int64_t)B * n_rt * Hkv * c <= device_sm_count() && stream_tiles <= (int64_t)c * tree::kClusterTiles) pl.cluster = c;
+    if (dtype == kBF16)
+        for (int i = 0; i < 3; ++i)
+            if ((int64_t)B * n_rt * Hkv <= room[i] && stream_tiles <= (int64_t)tree::kClusterTiles << (i + 1))
+                pl.cluster = 2 << i;
     if (pl.cluster) {
         pl.heads = pl.groups = 1;
         pl.ml_off = pl.o_off = pl.ws_bytes = 0;
@@ -428,7 +430,7 @@ bool make_tree_plan(int32_t B, int32_t N, int64_t max_len, int Hq, int Hkv, int 
     const int64_t blocks = (int64_t)B * n_rt * (Hkv / pl.heads);
     const int64_t tiles = blocks * stream_tiles;
     if ((int64_t)B * N * Hq > (int64_t)INT32_MAX / 2 || tiles > INT32_MAX / 2) return false;
-    const int64_t ctas = (int64_t)(dtype != kBF16 ? 2 : 1) * device_sm_count();
+    const int64_t ctas = (int64_t)(dtype != kBF16 ? 2 : 1) * sms;
     pl.groups = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, ctas / pl.heads));
     pl.ml_off = ((size_t)(B + 2) * sizeof(int32_t) + 15) / 16 * 16;
     const size_t entries = (size_t)pl.groups * pl.heads * 2 * pl.rows;

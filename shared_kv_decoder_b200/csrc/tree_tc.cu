@@ -25,7 +25,7 @@
 //                   a commit takes about a hundred cycles of its thread even when
 //                   nothing is left to wait for, and with one thread for both
 //                   chains these, not the tensor core, set the pace (16 x 64K-128K
-//                   tokens: 1115 us)
+//                   tokens on one box: 1180 us, 1074 with two threads in turns)
 // TMEM (512 columns): S_A/P_A, S_B/P_B, O_A, O_B, 128 columns each; P is bf16
 // over the first 64 columns of its S.
 //
@@ -208,11 +208,10 @@ YOCO_DEV void exp2_pair(float x0, float x1, float &e0, float &e1) {
     e1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23));
 }
 
-// Of every eight pairs of columns, how many take the FMA pipe.
-#ifndef TREE_POLY
-#define TREE_POLY 2
-#endif
-constexpr int kPoly = TREE_POLY;
+// Of every eight pairs of columns, how many take the FMA pipe.  64 x 48 nodes over
+// the 1024 ring: none 162 us, one 137, two 142, three 146, four 178 (the first and
+// last of an earlier build); the long contexts do not tell one from three.
+constexpr int kPoly = 1;
 
 // A ring segment's bounds over all its nodes: what every node sees and what
 // any does.

@@ -109,6 +109,29 @@ def test_rows_that_see_nothing(cuda_lib, dtype, most, N, Hq, Hkv, D):
 
 
 @pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("most", [128, 1 << 20])
+def test_no_nodes_at_all(cuda_lib, dtype, most):
+    lens = [100, 0]
+    q, kn, vn, kc, vc, starts = cross_case(dtype, lens, 3, 4, 2, 64, 450)
+    o, lse = run_cross(cuda_lib, q, kn, vn, kc, vc, starts, lens, None, [0, 0], max_len=most)
+    assert not o.any() and torch.isneginf(lse).all()
+    q, kn, vn, rk, rv, sp = ring_case(dtype, 2, 3, 40, [5, 90], 4, 2, 64, 460)
+    o, lse = run_swa(cuda_lib, q, kn, vn, [[5, 6, 7], [90, 91, 92]], rk, rv, sp, 40, None, [0, 0])
+    assert not o.any() and torch.isneginf(lse).all()
+
+
+@pytest.mark.parametrize("B,L", [(2, 4096), (14, 300), (30, 900)])
+def test_clusters_of_every_size(cuda_lib, B, L):
+    """Streams for clusters of eight, four and two CTAs."""
+    Hq, Hkv, D, N = 4, 1, 128, 6
+    lens = [L - 37 * b % L for b in range(B)]
+    assert cuda_lib.cross_decode_tree_workspace_size(B, N, L, Hq, Hkv, D, BF) == 0
+    q, kn, vn, kc, vc, starts = cross_case(BF, lens, N, Hq, Hkv, D, 470)
+    ref = tr.cross_tree(q, kn, vn, kc, vc, starts, lens)
+    tr.assert_tree(*run_cross(cuda_lib, q, kn, vn, kc, vc, starts, lens, max_len=L), ref, BF)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
 @pytest.mark.parametrize("most", [256, 1 << 20])
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
 @pytest.mark.parametrize("N,Hq,Hkv,D", [(5, 4, 2, 64), (40, 8, 2, 128)])
