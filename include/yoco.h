@@ -397,8 +397,9 @@ size_t yoco_swa_decode_tree_workspace_size(int32_t B, int32_t N, int32_t window,
  * int32 [B]; nodes path[b][0 .. n_path[b]) in order (later entries are not
  * read).  A sequence out of range (n_path outside [0, N], an entry outside
  * [0, N), or as stated below) is left as it is, and the next
- * yoco_get_device_status returns YOCO_ERR_INVALID.  cfg->Hq and cfg->scale
- * are not read beyond the usual checks.
+ * yoco_get_device_status returns YOCO_ERR_INVALID.  k_nodes and v_nodes do not
+ * overlap what is written.  cfg->Hq and cfg->scale are not read beyond the usual
+ * checks.
  *
  * yoco_cross_tree_commit: node path[j]'s K / V become cache row seq_start +
  * seq_len + j, and new_len[b] (device int32 [B], not seq_len itself) =

@@ -484,6 +484,8 @@ def _cuda_float(t, name):
         raise ValueError("libyoco takes CUDA tensors only")
     if t.dtype not in _DT:
         raise ValueError(f"{name}: {t.dtype}, expected {' or '.join(str(d) for d in _DT)}")
+    if not t.is_contiguous():
+        raise ValueError("libyoco takes contiguous tensors only")
     return t.get_device()
 
 
@@ -502,7 +504,7 @@ def _addr(t):
 def _call(device, name, *args):
     """A library call on CUDA device `device` and its current stream."""
     fn = getattr(_LIB or load(), name)
-    if device == torch.cuda.current_device():
+    if device == torch._C._cuda_getDevice():
         status = fn(*args, torch._C._cuda_getCurrentRawStream(device))
     else:
         with torch.cuda.device(device):
@@ -547,7 +549,6 @@ def rope(q, k, rope_cfg, pos=None, pos0=0, q_out=None, k_out=None, backward=Fals
         raise ValueError("rope takes [B, T, heads, D] or [B, heads, D]")
     Hkv = Hq
     if q is not None:
-        _want(q, "q", dtype, shape, device)
         if q_out is None:
             q_out = torch.empty_like(q)
         elif q_out is not q:
@@ -555,8 +556,9 @@ def rope(q, k, rope_cfg, pos=None, pos0=0, q_out=None, k_out=None, backward=Fals
     elif q_out is not None:
         raise ValueError("q_out without q")
     if k is not None:
-        Hkv = k.shape[-2] if k.dim() == len(shape) else -1
-        _want(k, "k", dtype, (*lead, Hkv, D), device)
+        if k is not x:
+            Hkv = k.shape[-2] if k.dim() == len(shape) else -1
+            _want(k, "k", dtype, (*lead, Hkv, D), device)
         if k_out is None:
             k_out = torch.empty_like(k)
         elif k_out is not k:
@@ -594,7 +596,6 @@ def _tree_args(q, k_nodes, v_nodes, tree_mask, n_nodes, context, workspace, o, w
     B, N, Hq, D = shape
     Hkv = k_nodes.shape[2]
     nodes = (B, N, Hkv, D)
-    _want(q, "q", dtype, shape, device)
     _want(k_nodes, "k_nodes", dtype, nodes, device)
     _want(v_nodes, "v_nodes", dtype, nodes, device)
     if tree_mask is not None:
@@ -662,7 +663,6 @@ def _commit_args(k_nodes, v_nodes, path, n_path):
     if k_nodes.dim() != 4:
         raise ValueError("k_nodes and v_nodes are [B, N, Hkv, D]")
     B, N = k_nodes.shape[:2]
-    _want(k_nodes, "k_nodes", k_nodes.dtype, k_nodes.shape, device)
     _want(v_nodes, "v_nodes", k_nodes.dtype, k_nodes.shape, device)
     _want(path, "path", _I32, (B, N), device)
     _want(n_path, "n_path", _I32, (B,), device)

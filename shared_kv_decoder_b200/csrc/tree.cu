@@ -27,7 +27,10 @@ constexpr int kSimtRows = 32;     // RS of the CUDA-core kernel
 constexpr int kSimtKeys = 64;     // BN of the CUDA-core kernel
 constexpr int kMergeWarps = 8;
 constexpr int kGroupHeads = 8;
-constexpr int kClusterTiles = 16;    // tiles of a CTA of a cluster at most
+// tiles of a CTA of a cluster at most, by whether the clusters fill half the GPU
+// (16 nodes over 2 x 8000 tokens, 16 tiles in clusters on 64 SMs, 26.1 us, as
+// shares 23.7; over 4 x 7900, on 128 SMs, 27.3 and 33.6)
+constexpr int kClusterTiles = 16, kFewClusterTiles = 12;
 constexpr int64_t kFewRows = 4096;   // rows that four merge warps each still serve in about a wave
 
 template <typename T>
@@ -414,8 +417,9 @@ bool make_tree_plan(int32_t B, int32_t N, int64_t max_len, int Hq, int Hkv, int 
     pl.cluster = 0;
     if (dtype == kBF16)
         for (int i = 0; i < 3; ++i)
-            if ((int64_t)B * n_rt * Hkv <= room[i] && stream_tiles <= (int64_t)tree::kClusterTiles << (i + 1))
-                pl.cluster = 2 << i;
+            if (const int64_t streams = (int64_t)B * n_rt * Hkv, c = 2 << i;
+                streams <= room[i] && stream_tiles <= c * (streams * c * 2 >= sms ? tree::kClusterTiles : tree::kFewClusterTiles))
+                pl.cluster = (int)c;
     if (pl.cluster) {
         pl.heads = pl.groups = 1;
         pl.ml_off = pl.o_off = pl.ws_bytes = 0;
