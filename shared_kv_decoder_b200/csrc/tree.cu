@@ -14,6 +14,7 @@
 #include "tree.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace yoco {
 
@@ -31,7 +32,6 @@ constexpr int kGroupHeads = 8;
 // (16 nodes over 2 x 8000 tokens, 16 tiles in clusters on 64 SMs, 26.1 us, as
 // shares 23.7; over 4 x 7900, on 128 SMs, 27.3 and 33.6)
 constexpr int kClusterTiles = 16, kFewClusterTiles = 12;
-constexpr int64_t kFewRows = 4096;   // rows that four merge warps each still serve in about a wave
 
 template <typename T>
 YOCO_DEV void load16(const T *src, float *f) {
@@ -239,19 +239,19 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_co
     }
 }
 
-// Joins the partials of shared streams.  grid.x: a block of rows; grid.y: a
-// candidate stream of a head block -- every stream, or, where there are more
-// streams than shares, the one that share grid.y + 1 starts inside of (the first
-// of its shares to do so); grid.z: the head in its block.  D / 4 lanes have four
-// columns each of one row.  SPLIT warps share a row's partials: four where there
-// are few rows, so that a long stream's partials are all in flight at once.
-template <typename T, int D, bool RING, int RS, int BN, int SPLIT>
+// Joins the partials of shared streams.  A lane has one row, a warp 32 rows'
+// four columns at a time (COLS of those groups of four, a group apart from the
+// next warp's): partials are stored by column, so its loads are whole.  grid.x:
+// a block of 32 rows, and of columns; grid.y: a candidate stream of a head block
+// -- every stream, or, where there are more streams than shares, the one that
+// share grid.y + 1 starts inside of (the first of its shares to do so); grid.z:
+// the head in its block.
+template <typename T, int D, bool RING, int RS, int BN, int COLS>
 __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const __grid_constant__ Params p, const int by_stream) {
-    constexpr int LANES = D / 4, AHEAD = 4, ROWS = 32 * kMergeWarps / (LANES * SPLIT);
-    __shared__ float s_ml[SPLIT][ROWS][2];
-    __shared__ float4 s_o[SPLIT][ROWS][SPLIT > 1 ? LANES : 1];
-    const int sub = threadIdx.x % LANES, slot = threadIdx.x / LANES % ROWS, share = threadIdx.x / (LANES * ROWS);
-    const int r = (int)blockIdx.x * ROWS + slot, blocks = p.Hkv / p.heads;
+    constexpr int GROUPS = D / 4, AHEAD = 4, COL_BLOCKS = GROUPS / (COLS * kMergeWarps);
+    const int lane = threadIdx.x & 31;
+    const int sub = (int)blockIdx.x % COL_BLOCKS * COLS * kMergeWarps + (threadIdx.x >> 5);   // the first group
+    const int r = (int)blockIdx.x / COL_BLOCKS * 32 + lane, blocks = p.Hkv / p.heads;
     pdl_trigger();
     pdl_wait();
     const int T_all = p.prefix[p.B], part = p.prefix[p.B + 1];
@@ -286,21 +286,24 @@ __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const __gr
     const int first = part > 0 || d.start(c0) == a ? 0 : 1, n_part = c1 - c0 + 1;
     const int g = stream % blocks * p.heads + (int)blockIdx.z, rr = stream / blocks * RS + r;
     const int node = rr >> p.lg, h = (g << p.lg) + (rr & ((1 << p.lg) - 1));
-    bool write = r < RS && node < s.n;
-    auto entry = [&](int i) { return (int64_t)((c0 + i) * p.heads + (int)blockIdx.z) * 2 + (i == 0 ? first : 0); };
+    if (r >= RS || node >= s.n) return;
     float M = -INFINITY, L = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = share; write && i0 < n_part; i0 += AHEAD * SPLIT) {
+    float4 acc[COLS];
+#pragma unroll
+    for (int c = 0; c < COLS; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < n_part; i0 += AHEAD) {
         float2 ml[AHEAD];
-        float4 o[AHEAD];
+        float4 o[AHEAD][COLS];
 #pragma unroll
         for (int u = 0; u < AHEAD; ++u) {
             ml[u] = make_float2(-INFINITY, 0.f);
-            o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (i0 + u * SPLIT < n_part) {
-                const int64_t e = entry(i0 + u * SPLIT);
+#pragma unroll
+            for (int c = 0; c < COLS; ++c) o[u][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i0 + u < n_part) {
+                const int64_t e = (int64_t)((c0 + i0 + u) * p.heads + (int)blockIdx.z) * 2 + (i0 + u == 0 ? first : 0);
                 ml[u] = p.ws_ml[e * RS + r];
-                o[u] = p.ws_o[(e * LANES + sub) * RS + r];
+#pragma unroll
+                for (int c = 0; c < COLS; ++c) o[u][c] = p.ws_o[(e * GROUPS + sub + c * kMergeWarps) * RS + r];
             }
         }
         float mx = M;
@@ -309,49 +312,33 @@ __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const __gr
         const float ref = mx == -INFINITY ? 0.f : mx;
         const float keep = exp2f(M - ref);
         L *= keep;
-        acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
+#pragma unroll
+        for (int c = 0; c < COLS; ++c)
+            acc[c] = make_float4(acc[c].x * keep, acc[c].y * keep, acc[c].z * keep, acc[c].w * keep);
 #pragma unroll
         for (int u = 0; u < AHEAD; ++u) {
             const float w = exp2f(ml[u].x - ref);
             L = fmaf(w, ml[u].y, L);
-            acc.x = fmaf(w, o[u].x, acc.x);
-            acc.y = fmaf(w, o[u].y, acc.y);
-            acc.z = fmaf(w, o[u].z, acc.z);
-            acc.w = fmaf(w, o[u].w, acc.w);
+#pragma unroll
+            for (int c = 0; c < COLS; ++c) {
+                acc[c].x = fmaf(w, o[u][c].x, acc[c].x);
+                acc[c].y = fmaf(w, o[u][c].y, acc[c].y);
+                acc[c].z = fmaf(w, o[u][c].z, acc[c].z);
+                acc[c].w = fmaf(w, o[u][c].w, acc[c].w);
+            }
         }
         M = mx;
     }
-    if constexpr (SPLIT > 1) {
-        if (sub == 0) {
-            s_ml[share][slot][0] = M;
-            s_ml[share][slot][1] = L;
-        }
-        s_o[share][slot][sub] = acc;
-        __syncthreads();
-        if (share != 0) return;
-#pragma unroll
-        for (int w = 1; w < SPLIT; ++w) M = fmaxf(M, s_ml[w][slot][0]);
-        const float ref = M == -INFINITY ? 0.f : M;
-        L = 0.f;
-        acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < SPLIT; ++w) {
-            const float f = exp2f(s_ml[w][slot][0] - ref);
-            const float4 o = s_o[w][slot][sub];
-            L = fmaf(f, s_ml[w][slot][1], L);
-            acc.x = fmaf(f, o.x, acc.x);
-            acc.y = fmaf(f, o.y, acc.y);
-            acc.z = fmaf(f, o.z, acc.z);
-            acc.w = fmaf(f, o.w, acc.w);
-        }
-    }
-    if (!write) return;
     const bool none = M == -INFINITY && L == 0.f;
     const float inv = none ? 0.f : 1.f / L;
-    T *dst = static_cast<T *>(p.o) + (((int64_t)b * p.N + node) * p.Hq + h) * D + 4 * sub;
-    const float v[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+    T *dst = static_cast<T *>(p.o) + (((int64_t)b * p.N + node) * p.Hq + h) * D;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) dst[e] = from_f32<T>(v[e]);
+    for (int c = 0; c < COLS; ++c) {
+        T v[4] = {from_f32<T>(acc[c].x * inv), from_f32<T>(acc[c].y * inv), from_f32<T>(acc[c].z * inv),
+                  from_f32<T>(acc[c].w * inv)};
+        using Out = std::conditional_t<sizeof(T) == 2, uint2, uint4>;
+        *reinterpret_cast<Out *>(dst + 4 * (sub + c * kMergeWarps)) = *reinterpret_cast<Out *>(v);
+    }
     if (p.lse && sub == 0)
         p.lse[((int64_t)b * p.Hq + h) * p.N + node] = none ? -INFINITY : (M + log2f(L)) * kLn2;
 }
@@ -376,11 +363,13 @@ cudaError_t launch_merge(const TreeArgs &a, const TreePlan &pl, cudaStream_t st)
     const bool by_stream = streams <= pl.groups - 1;
     const int most = by_stream ? (int)streams : pl.groups - 1;   // shared streams of a head
     if (most == 0) return cudaSuccess;                           // one share: nothing to join
-    const bool few = (int64_t)rows * most * pl.heads <= kFewRows;
-    const int per_cta = 32 * kMergeWarps / (D / 4) / (few ? 4 : 1);
+    // enough blocks of rows to fill the GPU: every column to one CTA; else spread
+    constexpr int ALL = D / 4 / kMergeWarps;
+    const int row_blocks = (rows + 31) / 32;
+    const bool whole = (int64_t)row_blocks * most * pl.heads >= 2 * device_sm_count();
     note_launches(1);
-    return launch_pdl(few ? tree_merge_kernel<T, D, RING, RS, BN, 4> : tree_merge_kernel<T, D, RING, RS, BN, 1>,
-                      dim3((unsigned)((rows + per_cta - 1) / per_cta), (unsigned)most, (unsigned)pl.heads),
+    return launch_pdl(whole ? tree_merge_kernel<T, D, RING, RS, BN, ALL> : tree_merge_kernel<T, D, RING, RS, BN, 1>,
+                      dim3((unsigned)(row_blocks * (whole ? 1 : ALL)), (unsigned)most, (unsigned)pl.heads),
                       dim3(32 * kMergeWarps), 0, st, make_params(a, pl), (int)by_stream);
 }
 
