@@ -16,12 +16,17 @@
 // more tiles a group (kAlignSlack) let every stream be cut into parts of `part`
 // tiles with no group holding pieces of two, it is cut so: a second segment
 // costs a CTA another fill and drain of its pipeline, as long as about five
-// tiles (4 sequences x 16 nodes over the 1024 ring: CTAs of one segment ran 11
-// us, those of two 17).  The streams are then numbered as if they were a
-// multiple of `part` long.  A CTA's part of a stream is a segment.  A stream that one CTA has whole is finished by it;
-// of one that is shared, each CTA leaves a partial (m, l, unnormalised o) in
-// the workspace, slot 0 for the segment its share opens with, slot 1 for the
-// one it ends with, and tree_merge_kernel joins them.
+// tiles (4 sequences x 16 nodes over the 1024 ring, before clusters took that
+// case: CTAs of one segment ran 11 us, those of two 17).  The streams are then
+// numbered as if they were a multiple of `part` long.  A CTA's part of a stream
+// is a segment.  A stream that one CTA has whole is finished by it; of one that
+// is shared, each CTA leaves a partial (m, l, unnormalised o) in the workspace,
+// slot 0 for the segment its share opens with, slot 1 for the one it ends with,
+// and tree_merge_kernel joins them.
+//
+// Few streams, none of them long, are not numbered: a cluster of CTAs has each,
+// and its CTAs join their parts through each other's shared memory (tree.cu says
+// when, tree_tc.cu how).
 #pragma once
 
 #include "common.cuh"

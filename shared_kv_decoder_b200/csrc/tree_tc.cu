@@ -8,11 +8,22 @@
 //         between two softmax warpgroups, each with its own S / P and O and its
 //         own running maximum; they are added up when the segment ends.
 //   PAIR  more rows: two row tiles (256 rows) read the same KV tile.
-// Either way two softmax chains interleave on every SM sub-partition while the
-// tensor core works for the other one.  What bounds it: with R rows of a KV
-// head a 64 KB K / V tile (D = 128) takes 4 * 128 * max(R, 128) * 128 tensor
-// operations; at the measured rates the cache read is the longer one up to about
-// R = 250.
+// Either way the tensor core works for one softmax chain while the other's
+// exponentials run.
+//
+// What bounds it.  With R rows of a KV head a 64 KB K / V tile (D = 128) takes
+// 4 * 128 * max(R, 128) * 128 tensor operations; at the measured rates the cache
+// read is the longer one up to about R = 250.  Measured (graph replays on
+// several boxes): 16 x 64K-128K tokens, 16 nodes (R = 64): 985-1100 us,
+// 5.8-6.4 TB/s of the cache, the clock at 1.3-1.5 GHz under the power cap;
+// 131007 tokens, 64 nodes (R = 256): 177-183 us, 750-780 TFLOP/s, the chain of
+// one tile's softmax (1950 cycles) and the MMAs that wait for it (2000) the
+// limit, tensor pipe 47% busy; 64 x 48 nodes over the 1024 ring: 132 us, a
+// segment's start and end (nine tiles) a quarter of it; in clusters 2047 tokens
+// 11.3 us, 4 x 16 nodes over the ring 13.2, latency throughout.
+// Two warps a row, 64 columns each, so that the softmax takes 1200 cycles, were
+// slower all the same (1050 for 1007 us, 155 for 142): the two have to agree on
+// the reference, and the power cap takes the rest.
 //
 // Warp roles (384 threads):
 //   warps 0-3, 4-7  softmax chains A and B: thread r owns row r (TMEM lane r)
