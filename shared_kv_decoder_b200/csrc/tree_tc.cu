@@ -14,7 +14,7 @@
 // What bounds it.  With R rows of a KV head a 64 KB K / V tile (D = 128) takes
 // 4 * 128 * max(R, 128) * 128 tensor operations; at the measured rates the cache
 // read is the longer one up to about R = 250.  Measured (graph replays on
-// several boxes): 16 x 64K-128K tokens, 16 nodes (R = 64): 985-1100 us,
+// several GPUs): 16 x 64K-128K tokens, 16 nodes (R = 64): 985-1100 us,
 // 5.8-6.4 TB/s of the cache, the clock at 1.3-1.5 GHz under the power cap;
 // 131007 tokens, 64 nodes (R = 256): 177-183 us, 750-780 TFLOP/s, the chain of
 // one tile's softmax (1950 cycles) and the MMAs that wait for it (2000) the
@@ -36,7 +36,7 @@
 //                   a commit takes about a hundred cycles of its thread even when
 //                   nothing is left to wait for, and with one thread for both
 //                   chains these, not the tensor core, set the pace (16 x 64K-128K
-//                   tokens on one box: 1180 us, 1074 with two threads in turns)
+//                   tokens on one GPU: 1180 us, 1074 with two threads in turns)
 // TMEM (512 columns): S_A/P_A, S_B/P_B, O_A, O_B, 128 columns each; P is bf16
 // over the first 64 columns of its S.
 //
