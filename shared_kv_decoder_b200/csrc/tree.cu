@@ -24,8 +24,8 @@ namespace tree {
 namespace {
 
 constexpr int kSimtThreads = 256;
-constexpr int kSimtRows = 32;     // RS of the CUDA-core kernel
-constexpr int kSimtKeys = 64;     // BN of the CUDA-core kernel
+constexpr int kFewRows = 8;       // RS of the CUDA-core kernel for few rows
+constexpr int kSimtKeys = 64;     // BN of the CUDA-core kernels
 constexpr int kMergeWarps = 8;
 constexpr int kGroupHeads = 8;
 // tiles of a CTA of a cluster at most, by whether the clusters fill half the GPU
@@ -33,106 +33,290 @@ constexpr int kGroupHeads = 8;
 // shares 23.7; over 4 x 7900, on 128 SMs, 27.3 and 33.6)
 constexpr int kClusterTiles = 16, kFewClusterTiles = 12;
 
-template <typename T>
-YOCO_DEV void load16(const T *src, float *f) {
-    Chunk<T>::unpack(*reinterpret_cast<const uint4 *>(src), f);
+// A tile of the fp32 kernels: where its keys are, and how many there are.
+struct Tile {
+    const float *k, *v;
+    int64_t row0;
+    int cnt, j0;
+    bool nodes;
+};
+YOCO_DEV Tile tile_of(const Params &p, const Seg &g, int t) {
+    Tile x;
+    x.nodes = t == g.n_ctx_tiles;
+    x.j0 = x.nodes ? 0 : t * kSimtKeys;
+    x.cnt = x.nodes ? g.n : min(kSimtKeys, g.ctx - x.j0);
+    x.row0 = x.nodes ? (int64_t)g.b * p.N : g.row0 + x.j0;
+    x.k = static_cast<const float *>(x.nodes ? p.k_nodes : p.k);
+    x.v = static_cast<const float *>(x.nodes ? p.v_nodes : p.v);
+    return x;
+}
+
+// Shared memory of a CTA: two stages of K and V rows (PITCH floats apart, which
+// keeps eight rows' chunks on different banks) and a ring's stored positions.
+template <int D>
+struct Stage {
+    static constexpr int PITCH = D + 4, FLOATS = 2 * kSimtKeys * PITCH;
+    float *k, *v;
+    int *slot;
+    YOCO_DEV Stage(float *base, int *slots, int i)
+        : k(base + (i & 1) * FLOATS), v(k + kSimtKeys * PITCH), slot(slots + (i & 1) * kSimtKeys) {}
+};
+
+// Starts the copy of a tile into a stage (rows past its keys as zeros).
+template <int D, bool RING>
+YOCO_DEV void load_tile(const Params &p, const Seg &g, int t, const Stage<D> &s) {
+    const Tile x = tile_of(p, g, t);
+    for (int c = threadIdx.x; c < kSimtKeys * (D / 4); c += kSimtThreads) {
+        const int j = c / (D / 4), d = (c % (D / 4)) * 4;
+        const bool there = j < x.cnt;
+        const int64_t off = there ? ((x.row0 + j) * p.Hkv + g.g) * D + d : 0;
+        const uint32_t bytes = there ? 16 : 0;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(s.k + j * Stage<D>::PITCH + d)),
+                     "l"(x.k + off), "r"(bytes) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(s.v + j * Stage<D>::PITCH + d)),
+                     "l"(x.v + off), "r"(bytes) : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    if (RING && !x.nodes && threadIdx.x < kSimtKeys)
+        s.slot[threadIdx.x] = threadIdx.x < x.cnt ? p.slot_pos[x.row0 + threadIdx.x] : -1;
+}
+
+// The rows of a row block: Q (scaled) into shared memory, what they see.
+template <int D, bool RING, int RS>
+YOCO_DEV void load_rows(const Params &p, const Seg &g, int rows, float *sq, uint64_t *s_nodes, RingBounds *s_bounds) {
+    const int G = 1 << p.lg;
+    for (int c = threadIdx.x; c < RS * (D / 4); c += kSimtThreads) {
+        const int r = c / (D / 4), d = (c % (D / 4)) * 4, rr = g.rt * RS + r;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < rows)
+            x = *reinterpret_cast<const float4 *>(
+                static_cast<const float *>(p.q) +
+                (((int64_t)g.b * p.N + (rr >> p.lg)) * p.Hq + (g.g << p.lg) + (rr & (G - 1))) * D + d);
+        *reinterpret_cast<float4 *>(sq + r * (D + 4) + d) =
+            make_float4(x.x * p.scale_log2, x.y * p.scale_log2, x.z * p.scale_log2, x.w * p.scale_log2);
+    }
+    if (threadIdx.x < RS) {
+        const int i = (g.rt * RS + (int)threadIdx.x) >> p.lg;
+        const bool there = (int)threadIdx.x < rows;
+        s_nodes[threadIdx.x] = there ? visible_nodes<RING>(p, g.b, g.n, i) : 0;
+        if (RING) s_bounds[threadIdx.x] = there ? ring_bounds(p.node_pos[(int64_t)g.b * p.N + i], p.window) : RingBounds{-1, -1};
+    }
+}
+
+// A finished row: to o and lse, or as a partial.
+template <int D, int RS>
+YOCO_DEV void store_four(const Params &p, const Seg &g, int r, int col4, float m, float L, float4 o) {
+    const int rr = g.rt * RS + r, node = rr >> p.lg, h = (g.g << p.lg) + (rr & ((1 << p.lg) - 1));
+    if (g.whole) {
+        const bool none = m == -INFINITY && L == 0.f;   // a NaN sum is not nothing
+        const float inv = none ? 0.f : 1.f / L;
+        *reinterpret_cast<float4 *>(static_cast<float *>(p.o) + (((int64_t)g.b * p.N + node) * p.Hq + h) * D + 4 * col4) =
+            make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+        if (p.lse && col4 == 0) p.lse[((int64_t)g.b * p.Hq + h) * p.N + node] = none ? -INFINITY : (m + log2f(L)) * kLn2;
+    } else {
+        const int64_t e = (int64_t)blockIdx.x * 2 + g.slot;
+        if (col4 == 0) p.ws_ml[e * RS + r] = make_float2(m, L);
+        p.ws_o[(e * (D / 4) + col4) * RS + r] = o;
+    }
 }
 
 }  // namespace
 
-// CUDA-core kernel: 256 threads for 32 rows x 64 keys.  Thread (ty, tx) of a
-// 16 x 16 grid holds rows 2 ty, 2 ty + 1: in S = q K^T the keys tx, tx + 16,
-// tx + 32, tx + 48; in O += P V the columns 4 tx + 64 j.  A row's statistics
-// are the same in its 16 threads.  P of a key that the row does not see is -1
-// in shared memory, and the product leaves such a key out, so what its K and V
-// hold (infinities, NaN) never reaches the row.
-template <typename T, int D, bool RING>
-__global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_constant__ Params p) {
-    constexpr int RS = kSimtRows, BN = kSimtKeys, PITCH = D + 4, PP = BN + 4;
-    constexpr int EPC = Chunk<T>::N, NJ = D / 64;
+// fp32 on the CUDA cores, up to eight rows of a KV head: bound by the cache read
+// (one tile computes while the next one's copies are on their way).  A warp has
+// four rows and sixteen keys of every tile, with statistics of its own, so that
+// nothing is exchanged before the segment ends: in S = q K^T lane (key, half of
+// D), in O += P V four columns a lane.  A key that a row does not see is left out
+// of the product (its weight is held as -1), so what its K and V hold never
+// reaches the row.
+template <int D, bool RING>
+__global__ void __launch_bounds__(kSimtThreads, 1) tree_few_kernel(const __grid_constant__ Params p) {
+    constexpr int RS = kFewRows, BN = kSimtKeys, PITCH = D + 4, CPL = D / 32;   // columns of a lane
     extern __shared__ __align__(16) float smem[];
-    float *sq = smem, *sk = sq + RS * PITCH, *sv = sk + BN * PITCH, *sp = sv + BN * PITCH;
     __shared__ Range s_range;
     __shared__ uint64_t s_nodes[RS];
-    __shared__ int s_slot[BN];
     __shared__ RingBounds s_bounds[RS];
+    __shared__ int s_slot[2 * BN];
+    __shared__ float2 s_ml[8][4];
+    float *sq = smem;
+    float *const stages = sq + RS * PITCH;
+    float *const red = stages;   // [8 warps][4 rows][D] when the segment ends
     pdl_trigger();
     pdl_wait();
     if (threadIdx.x < 32) find_range<RING, RS, BN>(p, &s_range);
     __syncthreads();
-    fill_rows_without_node<T, D, RING, RS, BN>(p, threadIdx.x / 32, kSimtThreads / 32, &g_status_tree);
-    const int G = 1 << p.lg;
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    fill_rows_without_node<float, D, RING, RS, BN>(p, threadIdx.x / 32, kSimtThreads / 32, &g_status_tree);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rq = (warp & 1) * 4, key = (warp >> 1) * 16 + (lane & 15), dh = lane >> 4;
     SegIter<RING, RS, BN> it(p, s_range);
     Seg g;
     while (it.next(p, g)) {
-        const int rows = min(RS, g.n * G - g.rt * RS);
+        const int rows = min(RS, (g.n << p.lg) - g.rt * RS);
+        load_tile<D, RING>(p, g, g.t0, Stage<D>(stages, s_slot, 0));
+        load_rows<D, RING, RS>(p, g, rows, sq, s_nodes, s_bounds);
+        float m[4], l[4], o[4][CPL];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            m[r] = -INFINITY;
+            l[r] = 0.f;
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) o[r][c] = 0.f;
+        }
+        for (int t = g.t0; t < g.t1; ++t) {
+            const Stage<D> cur(stages, s_slot, t - g.t0);
+            if (t + 1 < g.t1) {
+                load_tile<D, RING>(p, g, t + 1, Stage<D>(stages, s_slot, t + 1 - g.t0));
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+            } else {
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+            }
+            __syncthreads();
+            const Tile x = tile_of(p, g, t);
+            float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+            for (int d = 0; d < D / 2; d += 4) {
+                const float4 kk = *reinterpret_cast<const float4 *>(cur.k + key * PITCH + dh * (D / 2) + d);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float4 qq = *reinterpret_cast<const float4 *>(sq + (rq + r) * PITCH + dh * (D / 2) + d);
+                    s[r] = fmaf(qq.x, kk.x, s[r]);
+                    s[r] = fmaf(qq.y, kk.y, s[r]);
+                    s[r] = fmaf(qq.z, kk.z, s[r]);
+                    s[r] = fmaf(qq.w, kk.w, s[r]);
+                }
+            }
+            bool all = true;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                s[r] += __shfl_xor_sync(0xffffffffu, s[r], 16);
+                const bool see = x.nodes ? (s_nodes[rq + r] >> key) & 1
+                                 : RING  ? key < x.cnt && s_bounds[rq + r].sees(cur.slot[key])
+                                         : key < x.cnt;
+                all &= see;
+                // a NaN score has to reach the row: fmaxf would drop it, the exponential below does not
+                float mx = see ? fmaxf(m[r], s[r]) : m[r];
+#pragma unroll
+                for (int w = 8; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+                const float al = mx == -INFINITY ? 1.f : exp2f(m[r] - mx);
+                const float e = exp2f(s[r] - (mx == -INFINITY ? 0.f : mx));
+                m[r] = mx;
+                l[r] = l[r] * al + (see ? e : 0.f);
+#pragma unroll
+                for (int c = 0; c < CPL; ++c) o[r][c] *= al;
+                s[r] = see ? e : -1.f;
+            }
+            all = __all_sync(0xffffffffu, all);
+            const float *vrow = cur.v + (warp >> 1) * 16 * PITCH + lane * CPL;
+#pragma unroll 4
+            for (int k = 0; k < 16; ++k) {
+                float v[CPL];
+                if constexpr (CPL == 4) {
+                    const float4 y = *reinterpret_cast<const float4 *>(vrow + k * PITCH);
+                    v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
+                } else {
+                    const float2 y = *reinterpret_cast<const float2 *>(vrow + k * PITCH);
+                    v[0] = y.x, v[1] = y.y;
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float w = __shfl_sync(0xffffffffu, s[r], k);
+                    if (all || !(w < 0.f)) {   // seen (a NaN is)
+#pragma unroll
+                        for (int c = 0; c < CPL; ++c) o[r][c] = fmaf(w, v[c], o[r][c]);
+                    }
+                }
+            }
+            __syncthreads();   // before the stage is loaded again
+        }
+        // join the four key groups of each row
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+#pragma unroll
+            for (int w = 8; w > 0; w >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], w);
+            if (lane == 0) s_ml[warp][r] = make_float2(m[r], l[r]);
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) red[(warp * 4 + r) * D + lane * CPL + c] = o[r][c];
+        }
         __syncthreads();
-        for (int c = tid; c < RS * (D / EPC); c += kSimtThreads) {
-            const int r = c / (D / EPC), d = (c % (D / EPC)) * EPC;
-            float f[EPC];
+        if (warp < rows && lane < D / 4) {   // warp w writes row w
+            float M = -INFINITY, L = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int e = 0; e < EPC; ++e) f[e] = 0.f;
-            if (r < rows) {
-                const int rr = g.rt * RS + r;
-                load16(static_cast<const T *>(p.q) +
-                           (((int64_t)g.b * p.N + rr / G) * p.Hq + g.g * G + rr % G) * D + d, f);
+            for (int k = 0; k < 4; ++k) M = fmaxf(M, s_ml[2 * k + (warp >> 2)][warp & 3].x);
+            const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int from = 2 * k + (warp >> 2);
+                const float2 ml = s_ml[from][warp & 3];
+                const float w = exp2f(ml.x - ref);
+                const float4 y = *reinterpret_cast<const float4 *>(red + (from * 4 + (warp & 3)) * D + 4 * lane);
+                L = fmaf(w, ml.y, L);
+                acc.x = fmaf(w, y.x, acc.x);
+                acc.y = fmaf(w, y.y, acc.y);
+                acc.z = fmaf(w, y.z, acc.z);
+                acc.w = fmaf(w, y.w, acc.w);
             }
-#pragma unroll
-            for (int e = 0; e < EPC; ++e) sq[r * PITCH + d + e] = f[e] * p.scale_log2;
+            store_four<D, RS>(p, g, warp, lane, M, L, acc);
         }
-        if (tid < RS) {
-            const int i = (g.rt * RS + tid) / G;
-            s_nodes[tid] = tid < rows ? visible_nodes<RING>(p, g.b, g.n, i) : 0;
-            if (RING) {
-                if (tid < rows) s_bounds[tid] = ring_bounds(p.node_pos[(int64_t)g.b * p.N + i], p.window);
-                else s_bounds[tid] = RingBounds{-1, -1};
-            }
-        }
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[2][NJ * 4];
+        __syncthreads();   // before the next segment's first tile
+    }
+}
+
+// fp32 on the CUDA cores, more rows: bound by the FMA pipe.  256 threads for 16 RT
+// rows x 64 keys; thread (ty, tx) of a 16 x 16 grid holds rows RT ty .. RT ty +
+// RT - 1: in S = q K^T the keys tx, tx + 16, tx + 32, tx + 48; in O += P V the
+// columns 4 tx + 64 j.  A row's statistics are the same in its 16 threads; unseen
+// keys as in the kernel above.
+template <int D, bool RING, int RT>
+__global__ void __launch_bounds__(kSimtThreads, 1) tree_simt_kernel(const __grid_constant__ Params p) {
+    constexpr int RS = 16 * RT, BN = kSimtKeys, PITCH = D + 4, PP = BN + 4, NJ = D / 64;
+    extern __shared__ __align__(16) float smem[];
+    __shared__ Range s_range;
+    __shared__ uint64_t s_nodes[RS];
+    __shared__ RingBounds s_bounds[RS];
+    __shared__ int s_slot[2 * BN];
+    float *sq = smem, *sp = sq + RS * PITCH;
+    float *const stages = sp + RS * PP;
+    pdl_trigger();
+    pdl_wait();
+    if (threadIdx.x < 32) find_range<RING, RS, BN>(p, &s_range);
+    __syncthreads();
+    fill_rows_without_node<float, D, RING, RS, BN>(p, threadIdx.x / 32, kSimtThreads / 32, &g_status_tree);
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    SegIter<RING, RS, BN> it(p, s_range);
+    Seg g;
+    while (it.next(p, g)) {
+        const int rows = min(RS, (g.n << p.lg) - g.rt * RS);
+        load_tile<D, RING>(p, g, g.t0, Stage<D>(stages, s_slot, 0));
+        load_rows<D, RING, RS>(p, g, rows, sq, s_nodes, s_bounds);
+        float m[RT], l[RT], o[RT][NJ * 4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < RT; ++i) {
+            m[i] = -INFINITY;
+            l[i] = 0.f;
 #pragma unroll
             for (int e = 0; e < NJ * 4; ++e) o[i][e] = 0.f;
-
+        }
         for (int t = g.t0; t < g.t1; ++t) {
-            const bool nodes = t == g.n_ctx_tiles;
-            const int j0 = nodes ? 0 : t * BN;
-            const int cnt = nodes ? g.n : min(BN, g.ctx - j0);
-            const int64_t row0 = nodes ? (int64_t)g.b * p.N : g.row0 + j0;
-            const T *kb = static_cast<const T *>(nodes ? p.k_nodes : p.k);
-            const T *vb = static_cast<const T *>(nodes ? p.v_nodes : p.v);
-            __syncthreads();
-            for (int c = tid; c < BN * (D / EPC); c += kSimtThreads) {
-                const int j = c / (D / EPC), d = (c % (D / EPC)) * EPC;
-                float fk[EPC], fv[EPC];
-#pragma unroll
-                for (int e = 0; e < EPC; ++e) fk[e] = fv[e] = 0.f;
-                if (j < cnt) {
-                    const int64_t off = ((row0 + j) * p.Hkv + g.g) * D + d;
-                    load16(kb + off, fk);
-                    load16(vb + off, fv);
-                }
-#pragma unroll
-                for (int e = 0; e < EPC; e += 4) {
-                    *reinterpret_cast<float4 *>(sk + j * PITCH + d + e) = make_float4(fk[e], fk[e + 1], fk[e + 2], fk[e + 3]);
-                    *reinterpret_cast<float4 *>(sv + j * PITCH + d + e) = make_float4(fv[e], fv[e + 1], fv[e + 2], fv[e + 3]);
-                }
+            const Stage<D> cur(stages, s_slot, t - g.t0);
+            if (t + 1 < g.t1) {
+                load_tile<D, RING>(p, g, t + 1, Stage<D>(stages, s_slot, t + 1 - g.t0));
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+            } else {
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
             }
-            if (RING && !nodes && tid < BN)
-                s_slot[tid] = tid < cnt ? p.slot_pos[(int64_t)g.b * p.window + j0 + tid] : -1;
             __syncthreads();
-
-            float s[2][4] = {};
+            const Tile x = tile_of(p, g, t);
+            float s[RT][4] = {};
 #pragma unroll 4
             for (int d = 0; d < D; d += 4) {
-                float4 a[2], bk[4];
+                float4 a[RT], bk[4];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) a[i] = *reinterpret_cast<const float4 *>(sq + (2 * ty + i) * PITCH + d);
+                for (int i = 0; i < RT; ++i) a[i] = *reinterpret_cast<const float4 *>(sq + (RT * ty + i) * PITCH + d);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) bk[j] = *reinterpret_cast<const float4 *>(sk + (tx + 16 * j) * PITCH + d);
+                for (int j = 0; j < 4; ++j) bk[j] = *reinterpret_cast<const float4 *>(cur.k + (tx + 16 * j) * PITCH + d);
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < RT; ++i)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         s[i][j] = fmaf(a[i].x, bk[j].x, s[i][j]);
@@ -143,15 +327,15 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_co
             }
             bool all = true;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < RT; ++i) {
                 bool see[4];
                 float mx = m[i];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int c = tx + 16 * j;
-                    if (nodes) see[j] = (s_nodes[2 * ty + i] >> c) & 1;
-                    else if (RING) see[j] = c < cnt && s_bounds[2 * ty + i].sees(s_slot[c]);
-                    else see[j] = c < cnt;
+                    if (x.nodes) see[j] = (s_nodes[RT * ty + i] >> c) & 1;
+                    else if (RING) see[j] = c < x.cnt && s_bounds[RT * ty + i].sees(cur.slot[c]);
+                    else see[j] = c < x.cnt;
                     all &= see[j];
                     // a NaN score has to reach the row: fmaxf would drop it, the exponential below does not
                     if (see[j]) mx = fmaxf(mx, s[i][j]);
@@ -168,37 +352,43 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_co
                 for (int j = 0; j < 4; ++j) {
                     const float e = exp2f(s[i][j] - ref);
                     if (see[j]) l[i] += e;
-                    sp[(2 * ty + i) * PP + tx + 16 * j] = see[j] ? e : -1.f;
+                    sp[(RT * ty + i) * PP + tx + 16 * j] = see[j] ? e : -1.f;
                 }
             }
             all = __all_sync(0xffffffffu, all);
             __syncwarp();
             if (all) {
-#pragma unroll 4
-                for (int c = 0; c < BN; ++c) {
-                    const float p0 = sp[(2 * ty) * PP + c], p1 = sp[(2 * ty + 1) * PP + c];
+#pragma unroll 2
+                for (int c = 0; c < BN; c += 4) {
+                    float w[RT][4];
 #pragma unroll
-                    for (int j = 0; j < NJ; ++j) {
-                        const float4 v = *reinterpret_cast<const float4 *>(sv + c * PITCH + 4 * tx + 64 * j);
-                        o[0][4 * j] = fmaf(p0, v.x, o[0][4 * j]);
-                        o[0][4 * j + 1] = fmaf(p0, v.y, o[0][4 * j + 1]);
-                        o[0][4 * j + 2] = fmaf(p0, v.z, o[0][4 * j + 2]);
-                        o[0][4 * j + 3] = fmaf(p0, v.w, o[0][4 * j + 3]);
-                        o[1][4 * j] = fmaf(p1, v.x, o[1][4 * j]);
-                        o[1][4 * j + 1] = fmaf(p1, v.y, o[1][4 * j + 1]);
-                        o[1][4 * j + 2] = fmaf(p1, v.z, o[1][4 * j + 2]);
-                        o[1][4 * j + 3] = fmaf(p1, v.w, o[1][4 * j + 3]);
+                    for (int i = 0; i < RT; ++i) {
+                        const float4 y = *reinterpret_cast<const float4 *>(sp + (RT * ty + i) * PP + c);
+                        w[i][0] = y.x, w[i][1] = y.y, w[i][2] = y.z, w[i][3] = y.w;
                     }
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+#pragma unroll
+                        for (int j = 0; j < NJ; ++j) {
+                            const float4 v = *reinterpret_cast<const float4 *>(cur.v + (c + u) * PITCH + 4 * tx + 64 * j);
+#pragma unroll
+                            for (int i = 0; i < RT; ++i) {
+                                o[i][4 * j] = fmaf(w[i][u], v.x, o[i][4 * j]);
+                                o[i][4 * j + 1] = fmaf(w[i][u], v.y, o[i][4 * j + 1]);
+                                o[i][4 * j + 2] = fmaf(w[i][u], v.z, o[i][4 * j + 2]);
+                                o[i][4 * j + 3] = fmaf(w[i][u], v.w, o[i][4 * j + 3]);
+                            }
+                        }
                 }
             } else {
-                for (int c = 0; c < cnt; ++c) {
+                for (int c = 0; c < x.cnt; ++c) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float pp = sp[(2 * ty + i) * PP + c];
+                    for (int i = 0; i < RT; ++i) {
+                        const float pp = sp[(RT * ty + i) * PP + c];
                         if (pp < 0.f) continue;   // not seen (a NaN goes on)
 #pragma unroll
                         for (int j = 0; j < NJ; ++j) {
-                            const float4 v = *reinterpret_cast<const float4 *>(sv + c * PITCH + 4 * tx + 64 * j);
+                            const float4 v = *reinterpret_cast<const float4 *>(cur.v + c * PITCH + 4 * tx + 64 * j);
                             o[i][4 * j] = fmaf(pp, v.x, o[i][4 * j]);
                             o[i][4 * j + 1] = fmaf(pp, v.y, o[i][4 * j + 1]);
                             o[i][4 * j + 2] = fmaf(pp, v.z, o[i][4 * j + 2]);
@@ -207,34 +397,18 @@ __global__ void __launch_bounds__(kSimtThreads) tree_simt_kernel(const __grid_co
                     }
                 }
             }
+            __syncthreads();   // before the stage is loaded again
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < RT; ++i) {
             float L = l[i];
 #pragma unroll
             for (int w = 8; w > 0; w >>= 1) L += __shfl_xor_sync(0xffffffffu, L, w);
-            const int r = 2 * ty + i;
-            if (r >= rows) continue;
-            const int rr = g.rt * RS + r, node = rr / G, h = g.g * G + rr % G;
-            if (g.whole) {
-                const bool none = m[i] == -INFINITY && L == 0.f;   // a NaN sum is not nothing
-                const float inv = none ? 0.f : 1.f / L;
-                T *dst = static_cast<T *>(p.o) + (((int64_t)g.b * p.N + node) * p.Hq + h) * D;
+            if (RT * ty + i >= rows) continue;
 #pragma unroll
-                for (int j = 0; j < NJ; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) dst[4 * tx + 64 * j + e] = from_f32<T>(o[i][4 * j + e] * inv);
-                if (p.lse && tx == 0)
-                    p.lse[((int64_t)g.b * p.Hq + h) * p.N + node] =
-                        none ? -INFINITY : (m[i] + log2f(L)) * kLn2;
-            } else {
-                const int64_t e = (int64_t)blockIdx.x * 2 + g.slot;
-                if (tx == 0) p.ws_ml[e * RS + r] = make_float2(m[i], L);
-#pragma unroll
-                for (int j = 0; j < NJ; ++j)
-                    p.ws_o[(e * (D / 4) + tx + 16 * j) * RS + r] =
-                        make_float4(o[i][4 * j], o[i][4 * j + 1], o[i][4 * j + 2], o[i][4 * j + 3]);
-            }
+            for (int j = 0; j < NJ; ++j)
+                store_four<D, RS>(p, g, RT * ty + i, tx + 16 * j, m[i], L,
+                                  make_float4(o[i][4 * j], o[i][4 * j + 1], o[i][4 * j + 2], o[i][4 * j + 3]));
         }
     }
 }
@@ -346,10 +520,11 @@ __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const __gr
 // ------------------------------------------------------------------- host
 namespace {
 
-template <typename T, int D, bool RING>
-cudaError_t launch_simt(const TreeArgs &a, const TreePlan &pl, cudaStream_t st) {
-    constexpr size_t smem = sizeof(float) * ((kSimtRows + 2 * kSimtKeys) * (D + 4) + kSimtRows * (kSimtKeys + 4));
-    auto kern = tree_simt_kernel<T, D, RING>;
+template <int D, bool RING>
+cudaError_t launch_fp32(const TreeArgs &a, const TreePlan &pl, cudaStream_t st) {
+    const bool few = pl.rows == kFewRows;
+    const size_t smem = sizeof(float) * (pl.rows * (D + 4) + (few ? 0 : pl.rows * (kSimtKeys + 4)) + 2 * Stage<D>::FLOATS);
+    auto kern = few ? tree_few_kernel<D, RING> : pl.rows == 32 ? tree_simt_kernel<D, RING, 2> : tree_simt_kernel<D, RING, 4>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     note_launches(1);
@@ -381,9 +556,11 @@ cudaError_t launch_d(const TreeArgs &a, const TreePlan &pl, cudaStream_t st) {
         return pl.rows == 128 ? launch_merge<__nv_bfloat16, D, RING, 128, kTcKeys>(a, pl, st)
                               : launch_merge<__nv_bfloat16, D, RING, 256, kTcKeys>(a, pl, st);
     }
-    const cudaError_t e = launch_simt<float, D, RING>(a, pl, st);
+    const cudaError_t e = launch_fp32<D, RING>(a, pl, st);
     if (e != cudaSuccess) return e;
-    return launch_merge<float, D, RING, kSimtRows, kSimtKeys>(a, pl, st);
+    if (pl.rows == kFewRows) return launch_merge<float, D, RING, kFewRows, kSimtKeys>(a, pl, st);
+    return pl.rows == 32 ? launch_merge<float, D, RING, 32, kSimtKeys>(a, pl, st)
+                         : launch_merge<float, D, RING, 64, kSimtKeys>(a, pl, st);
 }
 
 }  // namespace
@@ -391,8 +568,10 @@ cudaError_t launch_d(const TreeArgs &a, const TreePlan &pl, cudaStream_t st) {
 
 bool make_tree_plan(int32_t B, int32_t N, int64_t max_len, int Hq, int Hkv, int D, int dtype, TreePlan *plan) {
     TreePlan pl;
-    // bf16: the tensor-core kernel, one row tile of 128 or two; fp32: CUDA cores
-    pl.rows = dtype != kBF16 ? tree::kSimtRows : N * (Hq / Hkv) <= 128 ? 128 : 256;
+    // bf16: the tensor-core kernel, one row tile of 128 or two; fp32: CUDA cores, in
+    // row blocks of 8, 32 or 64
+    const int R = N * (Hq / Hkv);
+    pl.rows = dtype == kBF16 ? R <= 128 ? 128 : 256 : R <= tree::kFewRows ? tree::kFewRows : R <= 32 ? 32 : 64;
     pl.keys = dtype != kBF16 ? tree::kSimtKeys : tree::kTcKeys;
     const int n_rt = (N * (Hq / Hkv) + pl.rows - 1) / pl.rows;
     const int64_t stream_tiles = (max_len + pl.keys - 1) / pl.keys + 1;
@@ -423,8 +602,7 @@ bool make_tree_plan(int32_t B, int32_t N, int64_t max_len, int Hq, int Hkv, int 
     const int64_t blocks = (int64_t)B * n_rt * (Hkv / pl.heads);
     const int64_t tiles = blocks * stream_tiles;
     if ((int64_t)B * N * Hq > (int64_t)INT32_MAX / 2 || tiles > INT32_MAX / 2) return false;
-    const int64_t ctas = (int64_t)(dtype != kBF16 ? 2 : 1) * sms;
-    pl.groups = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, ctas / pl.heads));
+    pl.groups = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, sms / pl.heads));
     pl.ml_off = ((size_t)(B + 2) * sizeof(int32_t) + 15) / 16 * 16;
     const size_t entries = (size_t)pl.groups * pl.heads * 2 * pl.rows;
     pl.o_off = pl.ml_off + entries * sizeof(float2);
