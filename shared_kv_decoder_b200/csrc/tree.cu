@@ -24,7 +24,8 @@ namespace tree {
 namespace {
 
 constexpr int kSimtThreads = 256;
-constexpr int kFewRows = 8;       // RS of the CUDA-core kernel for few rows
+constexpr int kFewRows = 16;      // RS of the CUDA-core kernel for few rows at most
+constexpr int kFewStages = 3;
 constexpr int kSimtKeys = 64;     // BN of the CUDA-core kernels
 constexpr int kMergeWarps = 8;
 constexpr int kGroupHeads = 8;
@@ -51,7 +52,7 @@ YOCO_DEV Tile tile_of(const Params &p, const Seg &g, int t) {
     return x;
 }
 
-// Shared memory of a CTA: two stages of K and V rows (PITCH floats apart, which
+// Shared memory of a CTA: stages of K and V rows (PITCH floats apart, which
 // keeps eight rows' chunks on different banks) and a ring's stored positions.
 template <int D>
 struct Stage {
@@ -59,7 +60,7 @@ struct Stage {
     float *k, *v;
     int *slot;
     YOCO_DEV Stage(float *base, int *slots, int i)
-        : k(base + (i & 1) * FLOATS), v(k + kSimtKeys * PITCH), slot(slots + (i & 1) * kSimtKeys) {}
+        : k(base + i * FLOATS), v(k + kSimtKeys * PITCH), slot(slots + i * kSimtKeys) {}
 };
 
 // Starts the copy of a tile into a stage (rows past its keys as zeros).
@@ -122,94 +123,130 @@ YOCO_DEV void store_four(const Params &p, const Seg &g, int r, int col4, float m
 
 }  // namespace
 
-// fp32 on the CUDA cores, up to eight rows of a KV head: bound by the cache read
-// (one tile computes while the next one's copies are on their way).  A warp has
-// four rows and sixteen keys of every tile, with statistics of its own, so that
-// nothing is exchanged before the segment ends: in S = q K^T lane (key, half of
-// D), in O += P V four columns a lane.  A key that a row does not see is left out
-// of the product (its weight is held as -1), so what its K and V hold never
-// reaches the row.
-template <int D, bool RING>
+// fp32 on the CUDA cores, few rows of a KV head: bound by the cache read (two
+// tiles are on their way while one computes).  A warp has eight rows and KW keys
+// of every tile, with statistics of its own, so that nothing is exchanged before
+// the segment ends.  S = q K^T: lane (key, one of DS parts of D), every row; the
+// parts' sums are exchanged so that a lane ends with the scores of 8 / DS rows.
+// O += P V: four columns a lane, the weights from shared memory.  A key that a row
+// does not see is left out of the product (its weight is held as -1), so what its
+// K and V hold never reaches the row.
+template <int D, bool RING, int RS>
 __global__ void __launch_bounds__(kSimtThreads, 1) tree_few_kernel(const __grid_constant__ Params p) {
-    constexpr int RS = kFewRows, BN = kSimtKeys, PITCH = D + 4, CPL = D / 32;   // columns of a lane
+    constexpr int BN = kSimtKeys, PITCH = D + 4, CPL = D / 32;   // columns of a lane
+    constexpr int RG = RS / 8, KG = 8 / RG, KW = BN / KG, DS = 32 / KW, DP = D / DS, MY = 8 / DS;
     extern __shared__ __align__(16) float smem[];
     __shared__ Range s_range;
     __shared__ uint64_t s_nodes[RS];
     __shared__ RingBounds s_bounds[RS];
-    __shared__ int s_slot[2 * BN];
-    __shared__ float2 s_ml[8][4];
-    float *sq = smem;
-    float *const stages = sq + RS * PITCH;
-    float *const red = stages;   // [8 warps][4 rows][D] when the segment ends
+    __shared__ int s_slot[kFewStages * BN];
+    __shared__ float2 s_ml[8][8];
+    float *sq = smem, *sw = sq + RS * PITCH;
+    float *const stages = sw + RG * BN * 8;
+    float *const red = stages;   // [8 warps][8 rows][D] when the segment ends
     pdl_trigger();
     pdl_wait();
     if (threadIdx.x < 32) find_range<RING, RS, BN>(p, &s_range);
     __syncthreads();
     fill_rows_without_node<float, D, RING, RS, BN>(p, threadIdx.x / 32, kSimtThreads / 32, &g_status_tree);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rq = (warp & 1) * 4, key = (warp >> 1) * 16 + (lane & 15), dh = lane >> 4;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, kg = warp / RG;
+    const int rq = warp % RG * 8, kl = lane % KW, key = kg * KW + kl, part = lane / KW;
+    const int mine = rq + part * MY;   // this lane's rows from here on, once the parts are joined
+    const float *const qp = sq + rq * PITCH + part * DP;
+    sw += warp * KW * 8;
     SegIter<RING, RS, BN> it(p, s_range);
     Seg g;
     while (it.next(p, g)) {
         const int rows = min(RS, (g.n << p.lg) - g.rt * RS);
-        load_tile<D, RING>(p, g, g.t0, Stage<D>(stages, s_slot, 0));
+        for (int i = 0; i < kFewStages - 1; ++i) {
+            if (g.t0 + i < g.t1) load_tile<D, RING>(p, g, g.t0 + i, Stage<D>(stages, s_slot, i));
+            else asm volatile("cp.async.commit_group;" ::: "memory");
+        }
         load_rows<D, RING, RS>(p, g, rows, sq, s_nodes, s_bounds);
-        float m[4], l[4], o[4][CPL];
+        float m[MY], l[MY], o[8][CPL];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
+        for (int r = 0; r < MY; ++r) {
             m[r] = -INFINITY;
             l[r] = 0.f;
+        }
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
 #pragma unroll
             for (int c = 0; c < CPL; ++c) o[r][c] = 0.f;
-        }
-        for (int t = g.t0; t < g.t1; ++t) {
-            const Stage<D> cur(stages, s_slot, t - g.t0);
-            if (t + 1 < g.t1) {
-                load_tile<D, RING>(p, g, t + 1, Stage<D>(stages, s_slot, t + 1 - g.t0));
-                asm volatile("cp.async.wait_group 1;" ::: "memory");
-            } else {
-                asm volatile("cp.async.wait_group 0;" ::: "memory");
-            }
-            __syncthreads();
+        for (int t = g.t0, st = 0; t < g.t1; ++t, st = st + 1 == kFewStages ? 0 : st + 1) {
+            const Stage<D> cur(stages, s_slot, st);
+            asm volatile("cp.async.wait_group %0;" ::"n"(kFewStages - 2) : "memory");
+            __syncthreads();   // this tile is here; the one before is no longer read
+            if (t + kFewStages - 1 < g.t1)
+                load_tile<D, RING>(p, g, t + kFewStages - 1, Stage<D>(stages, s_slot, st == 0 ? kFewStages - 1 : st - 1));
+            else asm volatile("cp.async.commit_group;" ::: "memory");
             const Tile x = tile_of(p, g, t);
-            float s[4] = {0.f, 0.f, 0.f, 0.f};
+            float s[8] = {};
+            const float *const kp = cur.k + key * PITCH + part * DP;
 #pragma unroll 4
-            for (int d = 0; d < D / 2; d += 4) {
-                const float4 kk = *reinterpret_cast<const float4 *>(cur.k + key * PITCH + dh * (D / 2) + d);
+            for (int d = 0; d < DP; d += 4) {
+                const float4 kk = *reinterpret_cast<const float4 *>(kp + d);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float4 qq = *reinterpret_cast<const float4 *>(sq + (rq + r) * PITCH + dh * (D / 2) + d);
+                for (int r = 0; r < 8; ++r) {
+                    const float4 qq = *reinterpret_cast<const float4 *>(qp + r * PITCH + d);
                     s[r] = fmaf(qq.x, kk.x, s[r]);
                     s[r] = fmaf(qq.y, kk.y, s[r]);
                     s[r] = fmaf(qq.z, kk.z, s[r]);
                     s[r] = fmaf(qq.w, kk.w, s[r]);
                 }
             }
-            bool all = true;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                s[r] += __shfl_xor_sync(0xffffffffu, s[r], 16);
-                const bool see = x.nodes ? (s_nodes[rq + r] >> key) & 1
-                                 : RING  ? key < x.cnt && s_bounds[rq + r].sees(cur.slot[key])
-                                         : key < x.cnt;
-                all &= see;
-                // a NaN score has to reach the row: fmaxf would drop it, the exponential below does not
-                float mx = see ? fmaxf(m[r], s[r]) : m[r];
+            for (int w = 16, n = 4; w >= KW; w >>= 1, n >>= 1) {
+                const bool upper = lane & w;
 #pragma unroll
-                for (int w = 8; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-                const float al = mx == -INFINITY ? 1.f : exp2f(m[r] - mx);
-                const float e = exp2f(s[r] - (mx == -INFINITY ? 0.f : mx));
-                m[r] = mx;
-                l[r] = l[r] * al + (see ? e : 0.f);
+                for (int r = 0; r < n; ++r) {
+                    const float there = __shfl_xor_sync(0xffffffffu, upper ? s[r] : s[r + n], w);
+                    s[r] = (upper ? s[r + n] : s[r]) + there;
+                }
+            }
+            bool see[MY], all = true, more = false;
 #pragma unroll
-                for (int c = 0; c < CPL; ++c) o[r][c] *= al;
-                s[r] = see ? e : -1.f;
+            for (int r = 0; r < MY; ++r) {
+                see[r] = x.nodes ? (s_nodes[mine + r] >> key) & 1
+                         : RING  ? key < x.cnt && s_bounds[mine + r].sees(cur.slot[key])
+                                 : key < x.cnt;
+                all &= see[r];
+                // a NaN score is not more, and reaches the row by its exponential
+                more |= see[r] && s[r] > m[r];
             }
             all = __all_sync(0xffffffffu, all);
-            const float *vrow = cur.v + (warp >> 1) * 16 * PITCH + lane * CPL;
+            if (__any_sync(0xffffffffu, more)) {   // a new maximum: rare after the first tiles
+                float al[MY];
+#pragma unroll
+                for (int r = 0; r < MY; ++r) {
+                    float mx = see[r] ? fmaxf(m[r], s[r]) : m[r];
+#pragma unroll
+                    for (int w = KW / 2; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+                    al[r] = mx == -INFINITY ? 1.f : exp2f(m[r] - mx);
+                    m[r] = mx;
+                    l[r] *= al[r];
+                }
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    const float f = __shfl_sync(0xffffffffu, al[r % MY], r / MY * KW);
+#pragma unroll
+                    for (int c = 0; c < CPL; ++c) o[r][c] *= f;
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < MY; ++r) {
+                const float e = exp2f(s[r] - (m[r] == -INFINITY ? 0.f : m[r]));
+                if (see[r]) l[r] += e;
+                s[r] = see[r] ? e : -1.f;
+            }
+#pragma unroll
+            for (int r = 0; r < MY; r += 2)
+                *reinterpret_cast<float2 *>(sw + kl * 8 + part * MY + r) = make_float2(s[r], s[r + 1]);
+            __syncwarp();
+            const float *const vrow = cur.v + kg * KW * PITCH + lane * CPL;
 #pragma unroll 4
-            for (int k = 0; k < 16; ++k) {
-                float v[CPL];
+            for (int k = 0; k < KW; ++k) {
+                float v[CPL], w[8];
                 if constexpr (CPL == 4) {
                     const float4 y = *reinterpret_cast<const float4 *>(vrow + k * PITCH);
                     v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
@@ -217,48 +254,50 @@ __global__ void __launch_bounds__(kSimtThreads, 1) tree_few_kernel(const __grid_
                     const float2 y = *reinterpret_cast<const float2 *>(vrow + k * PITCH);
                     v[0] = y.x, v[1] = y.y;
                 }
+                const float4 w0 = *reinterpret_cast<const float4 *>(sw + k * 8), w1 = *reinterpret_cast<const float4 *>(sw + k * 8 + 4);
+                w[0] = w0.x, w[1] = w0.y, w[2] = w0.z, w[3] = w0.w, w[4] = w1.x, w[5] = w1.y, w[6] = w1.z, w[7] = w1.w;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float w = __shfl_sync(0xffffffffu, s[r], k);
-                    if (all || !(w < 0.f)) {   // seen (a NaN is)
+                for (int r = 0; r < 8; ++r)
+                    if (all || !(w[r] < 0.f)) {   // seen (a NaN is)
 #pragma unroll
-                        for (int c = 0; c < CPL; ++c) o[r][c] = fmaf(w, v[c], o[r][c]);
+                        for (int c = 0; c < CPL; ++c) o[r][c] = fmaf(w[r], v[c], o[r][c]);
                     }
-                }
             }
-            __syncthreads();   // before the stage is loaded again
+            __syncwarp();   // before the weights are written again
         }
-        // join the four key groups of each row
+        __syncthreads();   // before the stages are used for the join
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
+        for (int r = 0; r < MY; ++r) {
 #pragma unroll
-            for (int w = 8; w > 0; w >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], w);
-            if (lane == 0) s_ml[warp][r] = make_float2(m[r], l[r]);
-#pragma unroll
-            for (int c = 0; c < CPL; ++c) red[(warp * 4 + r) * D + lane * CPL + c] = o[r][c];
+            for (int w = KW / 2; w > 0; w >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], w);
+            if (kl == 0) s_ml[warp][part * MY + r] = make_float2(m[r], l[r]);
         }
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) red[(warp * 8 + r) * D + lane * CPL + c] = o[r][c];
         __syncthreads();
-        if (warp < rows && lane < D / 4) {   // warp w writes row w
+        for (int r = warp; r < rows && lane < D / 4; r += 8) {   // the KG key groups of a row
             float M = -INFINITY, L = 0.f;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) M = fmaxf(M, s_ml[2 * k + (warp >> 2)][warp & 3].x);
+            for (int k = 0; k < KG; ++k) M = fmaxf(M, s_ml[k * RG + r / 8][r % 8].x);
             const float ref = M == -INFINITY ? 0.f : M;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int from = 2 * k + (warp >> 2);
-                const float2 ml = s_ml[from][warp & 3];
+            for (int k = 0; k < KG; ++k) {
+                const int from = k * RG + r / 8;
+                const float2 ml = s_ml[from][r % 8];
                 const float w = exp2f(ml.x - ref);
-                const float4 y = *reinterpret_cast<const float4 *>(red + (from * 4 + (warp & 3)) * D + 4 * lane);
+                const float4 y = *reinterpret_cast<const float4 *>(red + (from * 8 + r % 8) * D + 4 * lane);
                 L = fmaf(w, ml.y, L);
                 acc.x = fmaf(w, y.x, acc.x);
                 acc.y = fmaf(w, y.y, acc.y);
                 acc.z = fmaf(w, y.z, acc.z);
                 acc.w = fmaf(w, y.w, acc.w);
             }
-            store_four<D, RS>(p, g, warp, lane, M, L, acc);
+            store_four<D, RS>(p, g, r, lane, M, L, acc);
         }
-        __syncthreads();   // before the next segment's first tile
+        __syncthreads();   // before the next segment's first tiles
     }
 }
 
@@ -298,9 +337,9 @@ __global__ void __launch_bounds__(kSimtThreads, 1) tree_simt_kernel(const __grid
             for (int e = 0; e < NJ * 4; ++e) o[i][e] = 0.f;
         }
         for (int t = g.t0; t < g.t1; ++t) {
-            const Stage<D> cur(stages, s_slot, t - g.t0);
+            const Stage<D> cur(stages, s_slot, (t - g.t0) & 1);
             if (t + 1 < g.t1) {
-                load_tile<D, RING>(p, g, t + 1, Stage<D>(stages, s_slot, t + 1 - g.t0));
+                load_tile<D, RING>(p, g, t + 1, Stage<D>(stages, s_slot, (t + 1 - g.t0) & 1));
                 asm volatile("cp.async.wait_group 1;" ::: "memory");
             } else {
                 asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -522,9 +561,13 @@ namespace {
 
 template <int D, bool RING>
 cudaError_t launch_fp32(const TreeArgs &a, const TreePlan &pl, cudaStream_t st) {
-    const bool few = pl.rows == kFewRows;
-    const size_t smem = sizeof(float) * (pl.rows * (D + 4) + (few ? 0 : pl.rows * (kSimtKeys + 4)) + 2 * Stage<D>::FLOATS);
-    auto kern = few ? tree_few_kernel<D, RING> : pl.rows == 32 ? tree_simt_kernel<D, RING, 2> : tree_simt_kernel<D, RING, 4>;
+    const bool few = pl.rows <= kFewRows;
+    const size_t smem = sizeof(float) * (pl.rows * (D + 4) + (few ? pl.rows * kSimtKeys + kFewStages * Stage<D>::FLOATS
+                                                                  : pl.rows * (kSimtKeys + 4) + 2 * Stage<D>::FLOATS));
+    auto kern = pl.rows == 8    ? tree_few_kernel<D, RING, 8>
+                : pl.rows == 16 ? tree_few_kernel<D, RING, 16>
+                : pl.rows == 32 ? tree_simt_kernel<D, RING, 2>
+                                : tree_simt_kernel<D, RING, 4>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     note_launches(1);
@@ -558,9 +601,12 @@ cudaError_t launch_d(const TreeArgs &a, const TreePlan &pl, cudaStream_t st) {
     }
     const cudaError_t e = launch_fp32<D, RING>(a, pl, st);
     if (e != cudaSuccess) return e;
-    if (pl.rows == kFewRows) return launch_merge<float, D, RING, kFewRows, kSimtKeys>(a, pl, st);
-    return pl.rows == 32 ? launch_merge<float, D, RING, 32, kSimtKeys>(a, pl, st)
-                         : launch_merge<float, D, RING, 64, kSimtKeys>(a, pl, st);
+    switch (pl.rows) {
+        case 8: return launch_merge<float, D, RING, 8, kSimtKeys>(a, pl, st);
+        case 16: return launch_merge<float, D, RING, 16, kSimtKeys>(a, pl, st);
+        case 32: return launch_merge<float, D, RING, 32, kSimtKeys>(a, pl, st);
+        default: return launch_merge<float, D, RING, 64, kSimtKeys>(a, pl, st);
+    }
 }
 
 }  // namespace
@@ -569,9 +615,9 @@ cudaError_t launch_d(const TreeArgs &a, const TreePlan &pl, cudaStream_t st) {
 bool make_tree_plan(int32_t B, int32_t N, int64_t max_len, int Hq, int Hkv, int D, int dtype, TreePlan *plan) {
     TreePlan pl;
     // bf16: the tensor-core kernel, one row tile of 128 or two; fp32: CUDA cores, in
-    // row blocks of 8, 32 or 64
+    // row blocks of 8, 16, 32 or 64
     const int R = N * (Hq / Hkv);
-    pl.rows = dtype == kBF16 ? R <= 128 ? 128 : 256 : R <= tree::kFewRows ? tree::kFewRows : R <= 32 ? 32 : 64;
+    pl.rows = dtype == kBF16 ? R <= 128 ? 128 : 256 : R <= 8 ? 8 : R <= 16 ? 16 : R <= 32 ? 32 : 64;
     pl.keys = dtype != kBF16 ? tree::kSimtKeys : tree::kTcKeys;
     const int n_rt = (N * (Hq / Hkv) + pl.rows - 1) / pl.rows;
     const int64_t stream_tiles = (max_len + pl.keys - 1) / pl.keys + 1;
