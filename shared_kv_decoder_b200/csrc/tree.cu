@@ -23,10 +23,9 @@ static __device__ unsigned int g_status_tree;
 namespace tree {
 namespace {
 
-constexpr int kSimtThreads = 256;
-constexpr int kFewRows = 16;      // RS of the CUDA-core kernel for few rows at most
+constexpr int kFewThreads = 512, kRowThreads = 256;
 constexpr int kFewStages = 3;
-constexpr int kSimtKeys = 64;     // BN of the CUDA-core kernels
+constexpr int kSimtKeys = 64;   // BN of the CUDA-core kernels
 constexpr int kMergeWarps = 8;
 constexpr int kGroupHeads = 8;
 // tiles of a CTA of a cluster at most, by whether the clusters fill half the GPU
@@ -52,11 +51,11 @@ YOCO_DEV Tile tile_of(const Params &p, const Seg &g, int t) {
     return x;
 }
 
-// Shared memory of a CTA: stages of K and V rows (PITCH floats apart, which
-// keeps eight rows' chunks on different banks) and a ring's stored positions.
-template <int D>
+// Shared memory of a CTA: stages of K and V rows, PITCH floats apart, and of a
+// ring's stored positions.
+template <int PITCH>
 struct Stage {
-    static constexpr int PITCH = D + 4, FLOATS = 2 * kSimtKeys * PITCH;
+    static constexpr int FLOATS = 2 * kSimtKeys * PITCH;
     float *k, *v;
     int *slot;
     YOCO_DEV Stage(float *base, int *slots, int i)
@@ -64,17 +63,17 @@ struct Stage {
 };
 
 // Starts the copy of a tile into a stage (rows past its keys as zeros).
-template <int D, bool RING>
-YOCO_DEV void load_tile(const Params &p, const Seg &g, int t, const Stage<D> &s) {
+template <int D, bool RING, int THREADS, int PITCH>
+YOCO_DEV void load_tile(const Params &p, const Seg &g, int t, const Stage<PITCH> &s) {
     const Tile x = tile_of(p, g, t);
-    for (int c = threadIdx.x; c < kSimtKeys * (D / 4); c += kSimtThreads) {
+    for (int c = threadIdx.x; c < kSimtKeys * (D / 4); c += THREADS) {
         const int j = c / (D / 4), d = (c % (D / 4)) * 4;
         const bool there = j < x.cnt;
         const int64_t off = there ? ((x.row0 + j) * p.Hkv + g.g) * D + d : 0;
         const uint32_t bytes = there ? 16 : 0;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(s.k + j * Stage<D>::PITCH + d)),
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(s.k + j * PITCH + d)),
                      "l"(x.k + off), "r"(bytes) : "memory");
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(s.v + j * Stage<D>::PITCH + d)),
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(s.v + j * PITCH + d)),
                      "l"(x.v + off), "r"(bytes) : "memory");
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -83,17 +82,17 @@ YOCO_DEV void load_tile(const Params &p, const Seg &g, int t, const Stage<D> &s)
 }
 
 // The rows of a row block: Q (scaled) into shared memory, what they see.
-template <int D, bool RING, int RS>
+template <int D, bool RING, int RS, int THREADS, int PITCH>
 YOCO_DEV void load_rows(const Params &p, const Seg &g, int rows, float *sq, uint64_t *s_nodes, RingBounds *s_bounds) {
     const int G = 1 << p.lg;
-    for (int c = threadIdx.x; c < RS * (D / 4); c += kSimtThreads) {
+    for (int c = threadIdx.x; c < RS * (D / 4); c += THREADS) {
         const int r = c / (D / 4), d = (c % (D / 4)) * 4, rr = g.rt * RS + r;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         if (r < rows)
             x = *reinterpret_cast<const float4 *>(
                 static_cast<const float *>(p.q) +
                 (((int64_t)g.b * p.N + (rr >> p.lg)) * p.Hq + (g.g << p.lg) + (rr & (G - 1))) * D + d);
-        *reinterpret_cast<float4 *>(sq + r * (D + 4) + d) =
+        *reinterpret_cast<float4 *>(sq + r * PITCH + d) =
             make_float4(x.x * p.scale_log2, x.y * p.scale_log2, x.z * p.scale_log2, x.w * p.scale_log2);
     }
     if (threadIdx.x < RS) {
@@ -126,158 +125,157 @@ YOCO_DEV void store_four(const Params &p, const Seg &g, int r, int col4, float m
 // fp32 on the CUDA cores, few rows of a KV head: bound by the cache read (two
 // tiles are on their way while one computes).  A warp has eight rows and KW keys
 // of every tile, with statistics of its own, so that nothing is exchanged before
-// the segment ends.  S = q K^T: lane (key, one of DS parts of D), every row; the
-// parts' sums are exchanged so that a lane ends with the scores of 8 / DS rows.
-// O += P V: four columns a lane, the weights from shared memory.  A key that a row
-// does not see is left out of the product (its weight is held as -1), so what its
-// K and V hold never reaches the row.
+// the segment ends.  A lane has CPL columns of q, K, V and o, so that K and V are
+// read from shared memory once, in whole rows, and q stays in registers (with q
+// read from shared memory, where an operand that all lanes share costs as much as
+// one that they do not, one token over 8 x 8192 keys took 138 us).  The columns'
+// sums for four keys by eight rows are exchanged so that a lane ends with one of
+// the 32 scores: its q and K are loaded in an order that puts what it keeps first,
+// so that no exchange has to choose.  A key that a row does not see is left out of the product (its
+// weight is held as -1), so what its K and V hold never reaches the row.
 template <int D, bool RING, int RS>
-__global__ void __launch_bounds__(kSimtThreads, 1) tree_few_kernel(const __grid_constant__ Params p) {
-    constexpr int BN = kSimtKeys, PITCH = D + 4, CPL = D / 32;   // columns of a lane
-    constexpr int RG = RS / 8, KG = 8 / RG, KW = BN / KG, DS = 32 / KW, DP = D / DS, MY = 8 / DS;
+__global__ void __launch_bounds__(kFewThreads, 1) tree_few_kernel(const __grid_constant__ Params p) {
+    constexpr int BN = kSimtKeys, PITCH = D, CPL = D / 32, WARPS = kFewThreads / 32;
+    constexpr int RG = RS / 8, KG = WARPS / RG, KW = BN / KG;
+    using Cols = std::conditional_t<CPL == 4, float4, float2>;
+    union Lane {
+        Cols all;
+        float c[CPL];
+    };
     extern __shared__ __align__(16) float smem[];
     __shared__ Range s_range;
     __shared__ uint64_t s_nodes[RS];
     __shared__ RingBounds s_bounds[RS];
     __shared__ int s_slot[kFewStages * BN];
-    __shared__ float2 s_ml[8][8];
-    float *sq = smem, *sw = sq + RS * PITCH;
-    float *const stages = sw + RG * BN * 8;
-    float *const red = stages;   // [8 warps][8 rows][D] when the segment ends
+    __shared__ float2 s_ml[WARPS][8];
+    __shared__ __align__(16) float s_w[WARPS][4][8];
+    float *sq = smem;
+    float *const stages = sq + RS * PITCH;
+    float *const red = stages;   // [warp][8 rows][D] when the segment ends
     pdl_trigger();
     pdl_wait();
     if (threadIdx.x < 32) find_range<RING, RS, BN>(p, &s_range);
     __syncthreads();
-    fill_rows_without_node<float, D, RING, RS, BN>(p, threadIdx.x / 32, kSimtThreads / 32, &g_status_tree);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, kg = warp / RG;
-    const int rq = warp % RG * 8, kl = lane % KW, key = kg * KW + kl, part = lane / KW;
-    const int mine = rq + part * MY;   // this lane's rows from here on, once the parts are joined
-    const float *const qp = sq + rq * PITCH + part * DP;
-    sw += warp * KW * 8;
+    fill_rows_without_node<float, D, RING, RS, BN>(p, threadIdx.x / 32, WARPS, &g_status_tree);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, kg = warp / RG, rq = warp % RG * 8;
+    const int row = rq + (lane >> 2);   // of this lane's score
     SegIter<RING, RS, BN> it(p, s_range);
     Seg g;
     while (it.next(p, g)) {
         const int rows = min(RS, (g.n << p.lg) - g.rt * RS);
         for (int i = 0; i < kFewStages - 1; ++i) {
-            if (g.t0 + i < g.t1) load_tile<D, RING>(p, g, g.t0 + i, Stage<D>(stages, s_slot, i));
+            if (g.t0 + i < g.t1) load_tile<D, RING, kFewThreads, PITCH>(p, g, g.t0 + i, Stage<PITCH>(stages, s_slot, i));
             else asm volatile("cp.async.commit_group;" ::: "memory");
         }
-        load_rows<D, RING, RS>(p, g, rows, sq, s_nodes, s_bounds);
-        float m[MY], l[MY], o[8][CPL];
+        load_rows<D, RING, RS, kFewThreads, PITCH>(p, g, rows, sq, s_nodes, s_bounds);
+        __syncthreads();
+        float m = -INFINITY, l = 0.f;
+        float o[8][CPL];
+        Lane q[8];   // of row r ^ lane / 4
 #pragma unroll
-        for (int r = 0; r < MY; ++r) {
-            m[r] = -INFINITY;
-            l[r] = 0.f;
-        }
-#pragma unroll
-        for (int r = 0; r < 8; ++r)
+        for (int r = 0; r < 8; ++r) {
+            q[r].all = *reinterpret_cast<const Cols *>(sq + (rq + (r ^ lane >> 2)) * PITCH + lane * CPL);
 #pragma unroll
             for (int c = 0; c < CPL; ++c) o[r][c] = 0.f;
+        }
         for (int t = g.t0, st = 0; t < g.t1; ++t, st = st + 1 == kFewStages ? 0 : st + 1) {
-            const Stage<D> cur(stages, s_slot, st);
+            const Stage<PITCH> cur(stages, s_slot, st);
             asm volatile("cp.async.wait_group %0;" ::"n"(kFewStages - 2) : "memory");
             __syncthreads();   // this tile is here; the one before is no longer read
             if (t + kFewStages - 1 < g.t1)
-                load_tile<D, RING>(p, g, t + kFewStages - 1, Stage<D>(stages, s_slot, st == 0 ? kFewStages - 1 : st - 1));
+                load_tile<D, RING, kFewThreads, PITCH>(p, g, t + kFewStages - 1,
+                                                Stage<PITCH>(stages, s_slot, st == 0 ? kFewStages - 1 : st - 1));
             else asm volatile("cp.async.commit_group;" ::: "memory");
             const Tile x = tile_of(p, g, t);
-            float s[8] = {};
-            const float *const kp = cur.k + key * PITCH + part * DP;
-#pragma unroll 4
-            for (int d = 0; d < DP; d += 4) {
-                const float4 kk = *reinterpret_cast<const float4 *>(kp + d);
+#pragma unroll 1
+            for (int k0 = kg * KW; k0 < min((kg + 1) * KW, x.cnt); k0 += 4) {
+                float s[32];   // [row ^ lane / 4][key ^ lane % 4]
 #pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    const float4 qq = *reinterpret_cast<const float4 *>(qp + r * PITCH + d);
-                    s[r] = fmaf(qq.x, kk.x, s[r]);
-                    s[r] = fmaf(qq.y, kk.y, s[r]);
-                    s[r] = fmaf(qq.z, kk.z, s[r]);
-                    s[r] = fmaf(qq.w, kk.w, s[r]);
-                }
-            }
+                for (int k = 0; k < 4; ++k) {
+                    Lane kk;
+                    kk.all = *reinterpret_cast<const Cols *>(cur.k + (k0 + (k ^ (lane & 3))) * PITCH + lane * CPL);
 #pragma unroll
-            for (int w = 16, n = 4; w >= KW; w >>= 1, n >>= 1) {
-                const bool upper = lane & w;
+                    for (int r = 0; r < 8; ++r) {
+                        s[4 * r + k] = q[r].c[0] * kk.c[0];
 #pragma unroll
-                for (int r = 0; r < n; ++r) {
-                    const float there = __shfl_xor_sync(0xffffffffu, upper ? s[r] : s[r + n], w);
-                    s[r] = (upper ? s[r + n] : s[r]) + there;
-                }
-            }
-            bool see[MY], all = true, more = false;
-#pragma unroll
-            for (int r = 0; r < MY; ++r) {
-                see[r] = x.nodes ? (s_nodes[mine + r] >> key) & 1
-                         : RING  ? key < x.cnt && s_bounds[mine + r].sees(cur.slot[key])
-                                 : key < x.cnt;
-                all &= see[r];
-                // a NaN score is not more, and reaches the row by its exponential
-                more |= see[r] && s[r] > m[r];
-            }
-            all = __all_sync(0xffffffffu, all);
-            if (__any_sync(0xffffffffu, more)) {   // a new maximum: rare after the first tiles
-                float al[MY];
-#pragma unroll
-                for (int r = 0; r < MY; ++r) {
-                    float mx = see[r] ? fmaxf(m[r], s[r]) : m[r];
-#pragma unroll
-                    for (int w = KW / 2; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-                    al[r] = mx == -INFINITY ? 1.f : exp2f(m[r] - mx);
-                    m[r] = mx;
-                    l[r] *= al[r];
-                }
-#pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    const float f = __shfl_sync(0xffffffffu, al[r % MY], r / MY * KW);
-#pragma unroll
-                    for (int c = 0; c < CPL; ++c) o[r][c] *= f;
-                }
-            }
-#pragma unroll
-            for (int r = 0; r < MY; ++r) {
-                const float e = exp2f(s[r] - (m[r] == -INFINITY ? 0.f : m[r]));
-                if (see[r]) l[r] += e;
-                s[r] = see[r] ? e : -1.f;
-            }
-#pragma unroll
-            for (int r = 0; r < MY; r += 2)
-                *reinterpret_cast<float2 *>(sw + kl * 8 + part * MY + r) = make_float2(s[r], s[r + 1]);
-            __syncwarp();
-            const float *const vrow = cur.v + kg * KW * PITCH + lane * CPL;
-#pragma unroll 4
-            for (int k = 0; k < KW; ++k) {
-                float v[CPL], w[8];
-                if constexpr (CPL == 4) {
-                    const float4 y = *reinterpret_cast<const float4 *>(vrow + k * PITCH);
-                    v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
-                } else {
-                    const float2 y = *reinterpret_cast<const float2 *>(vrow + k * PITCH);
-                    v[0] = y.x, v[1] = y.y;
-                }
-                const float4 w0 = *reinterpret_cast<const float4 *>(sw + k * 8), w1 = *reinterpret_cast<const float4 *>(sw + k * 8 + 4);
-                w[0] = w0.x, w[1] = w0.y, w[2] = w0.z, w[3] = w0.w, w[4] = w1.x, w[5] = w1.y, w[6] = w1.z, w[7] = w1.w;
-#pragma unroll
-                for (int r = 0; r < 8; ++r)
-                    if (all || !(w[r] < 0.f)) {   // seen (a NaN is)
-#pragma unroll
-                        for (int c = 0; c < CPL; ++c) o[r][c] = fmaf(w[r], v[c], o[r][c]);
+                        for (int c = 1; c < CPL; ++c) s[4 * r + k] = fmaf(q[r].c[c], kk.c[c], s[4 * r + k]);
                     }
+                }
+#pragma unroll
+                for (int n = 16; n > 0; n >>= 1)
+#pragma unroll
+                    for (int i = 0; i < n; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i + n], n);
+                const float score = s[0];
+                const int key = k0 + (lane & 3);
+                const bool see = x.nodes ? (s_nodes[row] >> key) & 1
+                                 : RING  ? key < x.cnt && s_bounds[row].sees(cur.slot[key])
+                                         : key < x.cnt;
+                const bool all = __all_sync(0xffffffffu, see);
+                // a new maximum: rare after the first tiles (a NaN score is none, and
+                // reaches the row by its exponential)
+                if (__any_sync(0xffffffffu, see && score > m)) {
+                    float mx = see ? fmaxf(m, score) : m;
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                    const float al = mx == -INFINITY ? 1.f : exp2f(m - mx);
+                    m = mx;
+                    l *= al;
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) {
+                        const float f = __shfl_sync(0xffffffffu, al, 4 * r);
+#pragma unroll
+                        for (int c = 0; c < CPL; ++c) o[r][c] *= f;
+                    }
+                }
+                const float e = exp2f(score - (m == -INFINITY ? 0.f : m));
+                if (see) l += e;
+                __syncwarp();   // the last weights are read
+                s_w[warp][lane & 3][lane >> 2] = see ? e : -1.f;
+                __syncwarp();
+                if (all) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        Lane v;
+                        v.all = *reinterpret_cast<const Cols *>(cur.v + (k0 + k) * PITCH + lane * CPL);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float4 y = *reinterpret_cast<const float4 *>(&s_w[warp][k][4 * h]);
+                            const float w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                                for (int c = 0; c < CPL; ++c) o[4 * h + r][c] = fmaf(w[r], v.c[c], o[4 * h + r][c]);
+                        }
+                    }
+                } else {
+#pragma unroll 1
+                    for (int k = 0; k < 4; ++k) {
+                        Lane v;
+                        v.all = *reinterpret_cast<const Cols *>(cur.v + (k0 + k) * PITCH + lane * CPL);
+#pragma unroll
+                        for (int r = 0; r < 8; ++r) {
+                            const float w = s_w[warp][k][r];
+                            if (!(w < 0.f))   // seen (a NaN is)
+#pragma unroll
+                                for (int c = 0; c < CPL; ++c) o[r][c] = fmaf(w, v.c[c], o[r][c]);
+                        }
+                    }
+                }
             }
-            __syncwarp();   // before the weights are written again
         }
         __syncthreads();   // before the stages are used for the join
+        l += __shfl_xor_sync(0xffffffffu, l, 1);
+        l += __shfl_xor_sync(0xffffffffu, l, 2);
+        if ((lane & 3) == 0) s_ml[warp][lane >> 2] = make_float2(m, l);
 #pragma unroll
-        for (int r = 0; r < MY; ++r) {
+        for (int r = 0; r < 8; ++r) {
+            Lane x;
 #pragma unroll
-            for (int w = KW / 2; w > 0; w >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], w);
-            if (kl == 0) s_ml[warp][part * MY + r] = make_float2(m[r], l[r]);
+            for (int c = 0; c < CPL; ++c) x.c[c] = o[r][c];
+            *reinterpret_cast<Cols *>(red + (warp * 8 + r) * D + lane * CPL) = x.all;
         }
-#pragma unroll
-        for (int r = 0; r < 8; ++r)
-#pragma unroll
-            for (int c = 0; c < CPL; ++c) red[(warp * 8 + r) * D + lane * CPL + c] = o[r][c];
         __syncthreads();
-        for (int r = warp; r < rows && lane < D / 4; r += 8) {   // the KG key groups of a row
+        for (int r = warp; r < rows && lane < D / 4; r += WARPS) {   // the KG key groups of a row
             float M = -INFINITY, L = 0.f;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -307,8 +305,8 @@ __global__ void __launch_bounds__(kSimtThreads, 1) tree_few_kernel(const __grid_
 // columns 4 tx + 64 j.  A row's statistics are the same in its 16 threads; unseen
 // keys as in the kernel above.
 template <int D, bool RING, int RT>
-__global__ void __launch_bounds__(kSimtThreads, 1) tree_simt_kernel(const __grid_constant__ Params p) {
-    constexpr int RS = 16 * RT, BN = kSimtKeys, PITCH = D + 4, PP = BN + 4, NJ = D / 64;
+__global__ void __launch_bounds__(kRowThreads, 1) tree_simt_kernel(const __grid_constant__ Params p) {
+    constexpr int RS = 16 * RT, BN = kSimtKeys, PITCH = D + 4 /* eight keys on different banks */, PP = BN + 4, NJ = D / 64;
     extern __shared__ __align__(16) float smem[];
     __shared__ Range s_range;
     __shared__ uint64_t s_nodes[RS];
@@ -320,14 +318,14 @@ __global__ void __launch_bounds__(kSimtThreads, 1) tree_simt_kernel(const __grid
     pdl_wait();
     if (threadIdx.x < 32) find_range<RING, RS, BN>(p, &s_range);
     __syncthreads();
-    fill_rows_without_node<float, D, RING, RS, BN>(p, threadIdx.x / 32, kSimtThreads / 32, &g_status_tree);
+    fill_rows_without_node<float, D, RING, RS, BN>(p, threadIdx.x / 32, kRowThreads / 32, &g_status_tree);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     SegIter<RING, RS, BN> it(p, s_range);
     Seg g;
     while (it.next(p, g)) {
         const int rows = min(RS, (g.n << p.lg) - g.rt * RS);
-        load_tile<D, RING>(p, g, g.t0, Stage<D>(stages, s_slot, 0));
-        load_rows<D, RING, RS>(p, g, rows, sq, s_nodes, s_bounds);
+        load_tile<D, RING, kRowThreads, PITCH>(p, g, g.t0, Stage<PITCH>(stages, s_slot, 0));
+        load_rows<D, RING, RS, kRowThreads, PITCH>(p, g, rows, sq, s_nodes, s_bounds);
         float m[RT], l[RT], o[RT][NJ * 4];
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
@@ -337,9 +335,9 @@ __global__ void __launch_bounds__(kSimtThreads, 1) tree_simt_kernel(const __grid
             for (int e = 0; e < NJ * 4; ++e) o[i][e] = 0.f;
         }
         for (int t = g.t0; t < g.t1; ++t) {
-            const Stage<D> cur(stages, s_slot, (t - g.t0) & 1);
+            const Stage<PITCH> cur(stages, s_slot, (t - g.t0) & 1);
             if (t + 1 < g.t1) {
-                load_tile<D, RING>(p, g, t + 1, Stage<D>(stages, s_slot, (t + 1 - g.t0) & 1));
+                load_tile<D, RING, kRowThreads, PITCH>(p, g, t + 1, Stage<PITCH>(stages, s_slot, (t + 1 - g.t0) & 1));
                 asm volatile("cp.async.wait_group 1;" ::: "memory");
             } else {
                 asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -561,17 +559,17 @@ namespace {
 
 template <int D, bool RING>
 cudaError_t launch_fp32(const TreeArgs &a, const TreePlan &pl, cudaStream_t st) {
-    const bool few = pl.rows <= kFewRows;
-    const size_t smem = sizeof(float) * (pl.rows * (D + 4) + (few ? pl.rows * kSimtKeys + kFewStages * Stage<D>::FLOATS
-                                                                  : pl.rows * (kSimtKeys + 4) + 2 * Stage<D>::FLOATS));
+    const bool few = pl.rows <= 32;
+    const size_t smem = sizeof(float) * (few ? pl.rows * D + kFewStages * Stage<D>::FLOATS
+                                             : pl.rows * (D + 4 + kSimtKeys + 4) + 2 * Stage<D + 4>::FLOATS);
     auto kern = pl.rows == 8    ? tree_few_kernel<D, RING, 8>
                 : pl.rows == 16 ? tree_few_kernel<D, RING, 16>
-                : pl.rows == 32 ? tree_simt_kernel<D, RING, 2>
+                : pl.rows == 32 ? tree_few_kernel<D, RING, 32>
                                 : tree_simt_kernel<D, RING, 4>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     note_launches(1);
-    return launch_pdl(kern, dim3(pl.heads * pl.groups), dim3(kSimtThreads), smem, st, make_params(a, pl));
+    return launch_pdl(kern, dim3(pl.heads * pl.groups), dim3(few ? kFewThreads : kRowThreads), smem, st, make_params(a, pl));
 }
 
 template <typename T, int D, bool RING, int RS, int BN>
