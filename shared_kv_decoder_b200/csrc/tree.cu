@@ -62,8 +62,8 @@ struct Stage {
         : k(base + i * FLOATS), v(k + kSimtKeys * PITCH), slot(slots + i * kSimtKeys) {}
 };
 
-// Starts the copy of a tile into a stage (rows past its keys as zeros).
-template <int D, bool RING, int THREADS, int PITCH>
+// Starts the copy of a tile's K, V or both into a stage (rows past its keys as zeros).
+template <int D, bool RING, int THREADS, int PITCH, bool K, bool V>
 YOCO_DEV void load_tile(const Params &p, const Seg &g, int t, const Stage<PITCH> &s) {
     const Tile x = tile_of(p, g, t);
     for (int c = threadIdx.x; c < kSimtKeys * (D / 4); c += THREADS) {
@@ -71,13 +71,15 @@ YOCO_DEV void load_tile(const Params &p, const Seg &g, int t, const Stage<PITCH>
         const bool there = j < x.cnt;
         const int64_t off = there ? ((x.row0 + j) * p.Hkv + g.g) * D + d : 0;
         const uint32_t bytes = there ? 16 : 0;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(s.k + j * PITCH + d)),
-                     "l"(x.k + off), "r"(bytes) : "memory");
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(s.v + j * PITCH + d)),
-                     "l"(x.v + off), "r"(bytes) : "memory");
+        if (K)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(s.k + j * PITCH + d)),
+                         "l"(x.k + off), "r"(bytes) : "memory");
+        if (V)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(s.v + j * PITCH + d)),
+                         "l"(x.v + off), "r"(bytes) : "memory");
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
-    if (RING && !x.nodes && threadIdx.x < kSimtKeys)
+    if (RING && K && !x.nodes && threadIdx.x < kSimtKeys)
         s.slot[threadIdx.x] = threadIdx.x < x.cnt ? p.slot_pos[x.row0 + threadIdx.x] : -1;
 }
 
@@ -122,17 +124,21 @@ YOCO_DEV void store_four(const Params &p, const Seg &g, int r, int col4, float m
 
 }  // namespace
 
-// fp32 on the CUDA cores, few rows of a KV head: bound by the cache read (two
-// tiles are on their way while one computes).  A warp has eight rows and KW keys
-// of every tile, with statistics of its own, so that nothing is exchanged before
-// the segment ends.  A lane has CPL columns of q, K, V and o, so that K and V are
-// read from shared memory once, in whole rows, and q stays in registers (with q
-// read from shared memory, where an operand that all lanes share costs as much as
-// one that they do not, one token over 8 x 8192 keys took 138 us).  The columns'
-// sums for four keys by eight rows are exchanged so that a lane ends with one of
-// the 32 scores: its q and K are loaded in an order that puts what it keeps first,
-// so that no exchange has to choose.  A key that a row does not see is left out of the product (its
-// weight is held as -1), so what its K and V hold never reaches the row.
+// fp32 on the CUDA cores, up to 32 rows of a KV head: bound by issue slots, for
+// eight rows about as much by the cache read (two tiles are on their way while one
+// computes).  A warp has eight rows and KW keys of every tile, with statistics of
+// its own, so that nothing is exchanged before the segment ends.  A lane has CPL
+// columns of q, K, V and o: K and V are read from shared memory once, in whole
+// rows, and q stays in registers.  The columns' sums for four keys by eight rows
+// are exchanged so that a lane ends with one of the 32 scores; its q and K are
+// loaded in an order that puts what it keeps first, so that no exchange has to
+// choose.  A key that a row does not see is left out of the product (its weight is
+// held as -1), so what its K and V hold never reaches the row.
+// Over 8 x 8192 keys of 8 heads, D = 128: 8 rows take 116 us (4.6 TB/s), 16 take
+// 190, 32 take 315 (390 in the kernel below).  With a lane per key and q in shared
+// memory, where an operand that all lanes share costs as much as one that they do
+// not, 138, 221 and 368; with exchanges that choose, the same; with pairs of rows in
+// packed FMAs 155, 265 and 462.
 template <int D, bool RING, int RS>
 __global__ void __launch_bounds__(kFewThreads, 1) tree_few_kernel(const __grid_constant__ Params p) {
     constexpr int BN = kSimtKeys, PITCH = D, CPL = D / 32, WARPS = kFewThreads / 32;
@@ -164,7 +170,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) tree_few_kernel(const __grid_c
     while (it.next(p, g)) {
         const int rows = min(RS, (g.n << p.lg) - g.rt * RS);
         for (int i = 0; i < kFewStages - 1; ++i) {
-            if (g.t0 + i < g.t1) load_tile<D, RING, kFewThreads, PITCH>(p, g, g.t0 + i, Stage<PITCH>(stages, s_slot, i));
+            if (g.t0 + i < g.t1) load_tile<D, RING, kFewThreads, PITCH, true, true>(p, g, g.t0 + i, Stage<PITCH>(stages, s_slot, i));
             else asm volatile("cp.async.commit_group;" ::: "memory");
         }
         load_rows<D, RING, RS, kFewThreads, PITCH>(p, g, rows, sq, s_nodes, s_bounds);
@@ -183,7 +189,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) tree_few_kernel(const __grid_c
             asm volatile("cp.async.wait_group %0;" ::"n"(kFewStages - 2) : "memory");
             __syncthreads();   // this tile is here; the one before is no longer read
             if (t + kFewStages - 1 < g.t1)
-                load_tile<D, RING, kFewThreads, PITCH>(p, g, t + kFewStages - 1,
+                load_tile<D, RING, kFewThreads, PITCH, true, true>(p, g, t + kFewStages - 1,
                                                 Stage<PITCH>(stages, s_slot, st == 0 ? kFewStages - 1 : st - 1));
             else asm volatile("cp.async.commit_group;" ::: "memory");
             const Tile x = tile_of(p, g, t);
@@ -299,21 +305,24 @@ __global__ void __launch_bounds__(kFewThreads, 1) tree_few_kernel(const __grid_c
     }
 }
 
-// fp32 on the CUDA cores, more rows: bound by the FMA pipe.  256 threads for 16 RT
-// rows x 64 keys; thread (ty, tx) of a 16 x 16 grid holds rows RT ty .. RT ty +
-// RT - 1: in S = q K^T the keys tx, tx + 16, tx + 32, tx + 48; in O += P V the
-// columns 4 tx + 64 j.  A row's statistics are the same in its 16 threads; unseen
-// keys as in the kernel above.
+// fp32 on the CUDA cores, more rows: bound by reading operands from shared memory,
+// then by the FMA pipe.  256 threads for 16 RT rows x 64 keys; thread (ty, tx) of a
+// 16 x 16 grid holds the rows ty + 16 i: in S = q K^T the keys tx + 16 j, in O += P V
+// the columns 4 tx + 64 j.  V is copied while S is computed, the next K during P V.
+// A row's statistics are the same in its 16 threads; unseen keys as in the kernel
+// above.  64 nodes, G = 4, over 8 x 4096 keys: 932 us in blocks of 128 rows (37
+// TFLOP/s), 1052 in blocks of 64; 24 nodes 524 and about 600.
 template <int D, bool RING, int RT>
 __global__ void __launch_bounds__(kRowThreads, 1) tree_simt_kernel(const __grid_constant__ Params p) {
-    constexpr int RS = 16 * RT, BN = kSimtKeys, PITCH = D + 4 /* eight keys on different banks */, PP = BN + 4, NJ = D / 64;
+    constexpr int RS = 16 * RT, BN = kSimtKeys, NJ = D / 64;
+    constexpr int PITCH = D + 4, PP = BN + 16;   // eight keys, and two rows, on different banks
     extern __shared__ __align__(16) float smem[];
     __shared__ Range s_range;
     __shared__ uint64_t s_nodes[RS];
     __shared__ RingBounds s_bounds[RS];
-    __shared__ int s_slot[2 * BN];
+    __shared__ int s_slot[BN];
     float *sq = smem, *sp = sq + RS * PITCH;
-    float *const stages = sp + RS * PP;
+    const Stage<PITCH> cur(sp + RS * PP, s_slot, 0);
     pdl_trigger();
     pdl_wait();
     if (threadIdx.x < 32) find_range<RING, RS, BN>(p, &s_range);
@@ -324,7 +333,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) tree_simt_kernel(const __grid_
     Seg g;
     while (it.next(p, g)) {
         const int rows = min(RS, (g.n << p.lg) - g.rt * RS);
-        load_tile<D, RING, kRowThreads, PITCH>(p, g, g.t0, Stage<PITCH>(stages, s_slot, 0));
+        load_tile<D, RING, kRowThreads, PITCH, true, false>(p, g, g.t0, cur);
         load_rows<D, RING, RS, kRowThreads, PITCH>(p, g, rows, sq, s_nodes, s_bounds);
         float m[RT], l[RT], o[RT][NJ * 4];
 #pragma unroll
@@ -335,21 +344,16 @@ __global__ void __launch_bounds__(kRowThreads, 1) tree_simt_kernel(const __grid_
             for (int e = 0; e < NJ * 4; ++e) o[i][e] = 0.f;
         }
         for (int t = g.t0; t < g.t1; ++t) {
-            const Stage<PITCH> cur(stages, s_slot, (t - g.t0) & 1);
-            if (t + 1 < g.t1) {
-                load_tile<D, RING, kRowThreads, PITCH>(p, g, t + 1, Stage<PITCH>(stages, s_slot, (t + 1 - g.t0) & 1));
-                asm volatile("cp.async.wait_group 1;" ::: "memory");
-            } else {
-                asm volatile("cp.async.wait_group 0;" ::: "memory");
-            }
-            __syncthreads();
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            __syncthreads();   // K is here; the V before is no longer read
+            load_tile<D, RING, kRowThreads, PITCH, false, true>(p, g, t, cur);
             const Tile x = tile_of(p, g, t);
             float s[RT][4] = {};
 #pragma unroll 4
             for (int d = 0; d < D; d += 4) {
                 float4 a[RT], bk[4];
 #pragma unroll
-                for (int i = 0; i < RT; ++i) a[i] = *reinterpret_cast<const float4 *>(sq + (RT * ty + i) * PITCH + d);
+                for (int i = 0; i < RT; ++i) a[i] = *reinterpret_cast<const float4 *>(sq + (ty + 16 * i) * PITCH + d);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) bk[j] = *reinterpret_cast<const float4 *>(cur.k + (tx + 16 * j) * PITCH + d);
 #pragma unroll
@@ -370,8 +374,8 @@ __global__ void __launch_bounds__(kRowThreads, 1) tree_simt_kernel(const __grid_
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int c = tx + 16 * j;
-                    if (x.nodes) see[j] = (s_nodes[RT * ty + i] >> c) & 1;
-                    else if (RING) see[j] = c < x.cnt && s_bounds[RT * ty + i].sees(cur.slot[c]);
+                    if (x.nodes) see[j] = (s_nodes[ty + 16 * i] >> c) & 1;
+                    else if (RING) see[j] = c < x.cnt && s_bounds[ty + 16 * i].sees(cur.slot[c]);
                     else see[j] = c < x.cnt;
                     all &= see[j];
                     // a NaN score has to reach the row: fmaxf would drop it, the exponential below does not
@@ -389,18 +393,20 @@ __global__ void __launch_bounds__(kRowThreads, 1) tree_simt_kernel(const __grid_
                 for (int j = 0; j < 4; ++j) {
                     const float e = exp2f(s[i][j] - ref);
                     if (see[j]) l[i] += e;
-                    sp[(RT * ty + i) * PP + tx + 16 * j] = see[j] ? e : -1.f;
+                    sp[(ty + 16 * i) * PP + tx + 16 * j] = see[j] ? e : -1.f;
                 }
             }
             all = __all_sync(0xffffffffu, all);
-            __syncwarp();
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            __syncthreads();   // V is here; K is no longer read
+            if (t + 1 < g.t1) load_tile<D, RING, kRowThreads, PITCH, true, false>(p, g, t + 1, cur);
             if (all) {
 #pragma unroll 2
                 for (int c = 0; c < BN; c += 4) {
                     float w[RT][4];
 #pragma unroll
                     for (int i = 0; i < RT; ++i) {
-                        const float4 y = *reinterpret_cast<const float4 *>(sp + (RT * ty + i) * PP + c);
+                        const float4 y = *reinterpret_cast<const float4 *>(sp + (ty + 16 * i) * PP + c);
                         w[i][0] = y.x, w[i][1] = y.y, w[i][2] = y.z, w[i][3] = y.w;
                     }
 #pragma unroll
@@ -421,7 +427,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) tree_simt_kernel(const __grid_
                 for (int c = 0; c < x.cnt; ++c) {
 #pragma unroll
                     for (int i = 0; i < RT; ++i) {
-                        const float pp = sp[(RT * ty + i) * PP + c];
+                        const float pp = sp[(ty + 16 * i) * PP + c];
                         if (pp < 0.f) continue;   // not seen (a NaN goes on)
 #pragma unroll
                         for (int j = 0; j < NJ; ++j) {
@@ -434,17 +440,17 @@ __global__ void __launch_bounds__(kRowThreads, 1) tree_simt_kernel(const __grid_
                     }
                 }
             }
-            __syncthreads();   // before the stage is loaded again
         }
+        __syncthreads();   // before the next segment is loaded
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
             float L = l[i];
 #pragma unroll
             for (int w = 8; w > 0; w >>= 1) L += __shfl_xor_sync(0xffffffffu, L, w);
-            if (RT * ty + i >= rows) continue;
+            if (ty + 16 * i >= rows) continue;
 #pragma unroll
             for (int j = 0; j < NJ; ++j)
-                store_four<D, RS>(p, g, RT * ty + i, tx + 16 * j, m[i], L,
+                store_four<D, RS>(p, g, ty + 16 * i, tx + 16 * j, m[i], L,
                                   make_float4(o[i][4 * j], o[i][4 * j + 1], o[i][4 * j + 2], o[i][4 * j + 3]));
         }
     }
@@ -561,11 +567,12 @@ template <int D, bool RING>
 cudaError_t launch_fp32(const TreeArgs &a, const TreePlan &pl, cudaStream_t st) {
     const bool few = pl.rows <= 32;
     const size_t smem = sizeof(float) * (few ? pl.rows * D + kFewStages * Stage<D>::FLOATS
-                                             : pl.rows * (D + 4 + kSimtKeys + 4) + 2 * Stage<D + 4>::FLOATS);
+                                             : pl.rows * (D + 4 + kSimtKeys + 16) + Stage<D + 4>::FLOATS);
     auto kern = pl.rows == 8    ? tree_few_kernel<D, RING, 8>
                 : pl.rows == 16 ? tree_few_kernel<D, RING, 16>
                 : pl.rows == 32 ? tree_few_kernel<D, RING, 32>
-                                : tree_simt_kernel<D, RING, 4>;
+                : pl.rows == 64 ? tree_simt_kernel<D, RING, 4>
+                                : tree_simt_kernel<D, RING, 8>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     note_launches(1);
@@ -603,7 +610,8 @@ cudaError_t launch_d(const TreeArgs &a, const TreePlan &pl, cudaStream_t st) {
         case 8: return launch_merge<float, D, RING, 8, kSimtKeys>(a, pl, st);
         case 16: return launch_merge<float, D, RING, 16, kSimtKeys>(a, pl, st);
         case 32: return launch_merge<float, D, RING, 32, kSimtKeys>(a, pl, st);
-        default: return launch_merge<float, D, RING, 64, kSimtKeys>(a, pl, st);
+        case 64: return launch_merge<float, D, RING, 64, kSimtKeys>(a, pl, st);
+        default: return launch_merge<float, D, RING, 128, kSimtKeys>(a, pl, st);
     }
 }
 
@@ -613,9 +621,9 @@ cudaError_t launch_d(const TreeArgs &a, const TreePlan &pl, cudaStream_t st) {
 bool make_tree_plan(int32_t B, int32_t N, int64_t max_len, int Hq, int Hkv, int D, int dtype, TreePlan *plan) {
     TreePlan pl;
     // bf16: the tensor-core kernel, one row tile of 128 or two; fp32: CUDA cores, in
-    // row blocks of 8, 16, 32 or 64
+    // row blocks of 8, 16, 32, 64 or 128 (what they take: at the kernels)
     const int R = N * (Hq / Hkv);
-    pl.rows = dtype == kBF16 ? R <= 128 ? 128 : 256 : R <= 8 ? 8 : R <= 16 ? 16 : R <= 32 ? 32 : 64;
+    pl.rows = dtype == kBF16 ? R <= 128 ? 128 : 256 : R <= 8 ? 8 : R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128;
     pl.keys = dtype != kBF16 ? tree::kSimtKeys : tree::kTcKeys;
     const int n_rt = (N * (Hq / Hkv) + pl.rows - 1) / pl.rows;
     const int64_t stream_tiles = (max_len + pl.keys - 1) / pl.keys + 1;

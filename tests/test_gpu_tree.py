@@ -497,6 +497,32 @@ def test_graph_replay_and_two_streams(cuda_lib, dtype, most):
         tr.assert_tree(*outs[i], refs[i], dtype, f"stream {i}")
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("N,G", [(1, 1), (2, 4), (9, 1), (4, 4), (3, 8), (8, 4), (33, 1), (16, 4), (11, 8), (64, 2), (50, 4)])
+def test_fp32_row_blocks(cuda_lib, N, G, D):
+    """Every row block of the fp32 kernels, full and ragged: segments of many
+    tiles, keys whose scores grow along the sequence (so maxima keep moving), and
+    nodes that nobody sees, with NaN in K and V."""
+    lens, Hkv = [2300, 900, 1, 64], 2
+    q, kn, vn, kc, vc, starts = cross_case(FP, lens, N, Hkv * G, Hkv, D, 1500)
+    for s, n in zip(starts, lens):
+        kc[s:s + n] *= torch.linspace(0, 1, n)[:, None, None]
+    rng = np.random.default_rng(N)
+    masks = [tr.random_tree(rng, N)[0] for _ in lens]
+    for i in range(N):
+        masks[0][i] &= ~(1 << (N - 1))
+    masks[1] = [0] * N
+    kn[0, N - 1], vn[0, N - 1] = math.nan, math.nan
+    ref = tr.cross_tree(q, torch.nan_to_num(kn), torch.nan_to_num(vn), kc, vc, starts, lens, masks)
+    for most in (2300, 1 << 20):
+        tr.assert_tree(*run_cross(cuda_lib, q, kn, vn, kc, vc, starts, lens, masks, max_len=most), ref, FP)
+    B, W = 3, 200
+    q, kn, vn, rk, rv, sp = ring_case(FP, B, N, W, [150, 1000, 0], Hkv * G, Hkv, D, 1600)
+    pos = [[150 + i for i in range(N)], [1000 + 5 * i for i in range(N)], list(range(N))]
+    ref = tr.swa_tree(q, kn, vn, pos, rk, rv, sp, W)
+    tr.assert_tree(*run_swa(cuda_lib, q, kn, vn, pos, rk, rv, sp, W), ref, FP)
+
+
 def test_offsets_beyond_32_bits(cuda_lib):
     """Rows whose element offset passes 2^32 in a cache of 4.4e9 elements."""
     Hq, Hkv, D, N = 16, 16, 128, 3
