@@ -291,6 +291,11 @@ YOCO_DEV void fill_rows_without_node(const Params &p, int w, int warps, unsigned
 }
 
 // ------------------------------------------------------------- visibility
+// pos - window < at <= pos, whatever the two positions are.
+YOCO_DEV bool in_window(int64_t pos, int64_t at, int32_t window) {
+    return at <= pos && (uint64_t)pos - (uint64_t)at < (uint64_t)window;
+}
+
 // The nodes that node i of n sees, one bit each: the mask's (a chain's without
 // one), of those that exist, and for a ring those inside i's window.
 template <bool RING>
@@ -299,9 +304,9 @@ YOCO_DEV uint64_t visible_nodes(const Params &p, int b, int n, int i) {
     uint64_t w = p.mask ? p.mask[at + i] : (2ull << i) - 1;
     if (n < 64) w &= (1ull << n) - 1;
     if (RING) {
-        const uint64_t pos = (uint64_t)p.node_pos[at + i];
+        const int64_t pos = p.node_pos[at + i];
         for (int j = 0; j < n; ++j)
-            if (pos - (uint64_t)p.node_pos[at + j] >= (uint64_t)p.window) w &= ~(1ull << j);
+            if (!in_window(pos, p.node_pos[at + j], p.window)) w &= ~(1ull << j);
     }
     return w;
 }

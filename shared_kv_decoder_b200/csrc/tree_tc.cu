@@ -536,9 +536,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int i = 0; i < 32 >> p.lg; ++i) {
                             const int at = __shfl_sync(0xffffffffu, node, i << p.lg) & 63;
                             const int64_t m0 = __shfl_sync(0xffffffffu, p0, at & 31), m1 = __shfl_sync(0xffffffffu, p1, at & 31);
-                            const uint64_t mine = (uint64_t)(at < 32 ? m0 : m1);
-                            const uint32_t w0 = __ballot_sync(0xffffffffu, mine - (uint64_t)p0 < (uint64_t)p.window);
-                            const uint32_t w1 = __ballot_sync(0xffffffffu, mine - (uint64_t)p1 < (uint64_t)p.window);
+                            const int64_t mine = at < 32 ? m0 : m1;
+                            const uint32_t w0 = __ballot_sync(0xffffffffu, in_window(mine, p0, p.window));
+                            const uint32_t w1 = __ballot_sync(0xffffffffu, in_window(mine, p1, p.window));
                             if (lane >> p.lg == i) vis &= (uint64_t)w1 << 32 | w0;
                         }
                     }

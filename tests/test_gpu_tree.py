@@ -497,6 +497,21 @@ def test_graph_replay_and_two_streams(cuda_lib, dtype, most):
         tr.assert_tree(*outs[i], refs[i], dtype, f"stream {i}")
 
 
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_node_positions_at_both_ends(cuda_lib, dtype):
+    """A node near the largest position and one near the smallest do not see each other."""
+    N, W = 4, 8
+    q, kn, vn, rk, rv, sp = ring_case(dtype, 1, N, W, [5], 4, 2, 64, 780)
+    pos = [[-2 ** 63, 2 ** 63 - 1, 3, -2 ** 63 + 1]]
+    masks = [[15] * N]
+    # in the plain form as positions apart: node 0 and 3 see 0 (and 3 itself), 1 and 2 themselves
+    ref = tr.cross_tree(q[:, :2], kn[:, :2], vn[:, :2], kn[0, :0], vn[0, :0], [0], [0], [[1, 2]])
+    o, lse = run_swa(cuda_lib, q, kn, vn, pos, rk, rv, sp, W, masks)
+    tr.assert_tree(o[:, :2].contiguous(), lse[:, :, :2].contiguous(), ref, dtype)
+    ref = tr.cross_tree(q, kn, vn, kn[0, :0], vn[0, :0], [0], [0], [[1, 2, 4, 9]])
+    tr.assert_tree(o[:, 3:].contiguous(), lse[:, :, 3:].contiguous(), [x[:, 3:] if x.ndim == 4 else x[:, :, 3:] for x in ref], dtype)
+
+
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("N,G", [(1, 1), (2, 4), (9, 1), (4, 4), (3, 8), (8, 4), (33, 1), (16, 4), (11, 8), (64, 2), (50, 4)])
 def test_fp32_row_blocks(cuda_lib, N, G, D):
