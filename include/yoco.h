@@ -358,7 +358,7 @@ yoco_status yoco_rope(const void *q, const void *k, int32_t B, int64_t T, const 
  *    not exist; nothing sees them and their rows come out as below.
  *  - A row that sees no key, or whose node does not exist: o = 0, lse = -inf.
  *    What an unseen key's K and V hold (infinities, NaN) has no effect.
- *  - lse [B, Hq, N] or NULL.
+ *  - lse [B, Hq, N] or NULL.  o, lse and the workspace overlap no input.
  *  - workspace: device scratch of the size query's bytes, NULL where that says 0
  *    (few streams, none of them long: the CTAs of a cluster join their parts
  *    themselves); it needs no clearing and keeps nothing between calls, but
@@ -397,17 +397,18 @@ size_t yoco_swa_decode_tree_workspace_size(int32_t B, int32_t N, int32_t window,
  * int32 [B]; nodes path[b][0 .. n_path[b]) in order (later entries are not
  * read).  A sequence out of range (n_path outside [0, N], an entry outside
  * [0, N), or as stated below) is left as it is, and the next
- * yoco_get_device_status returns YOCO_ERR_INVALID.  k_nodes and v_nodes do not
- * overlap what is written.  cfg->Hq and cfg->scale are not read beyond the usual
- * checks.
+ * yoco_get_device_status returns YOCO_ERR_INVALID.  What is written overlaps no
+ * input (YOCO_ERR_INVALID where new_len or slot_pos overlaps a small one: a
+ * step that keeps its lengths in place swaps two buffers).  cfg->Hq and
+ * cfg->scale are not read beyond the usual checks.
  *
  * yoco_cross_tree_commit: node path[j]'s K / V become cache row seq_start +
- * seq_len + j, and new_len[b] (device int32 [B], not seq_len itself) =
- * seq_len + n_path.  seq_cap: device int32 [B], the most rows each sequence may
- * have, or NULL: the caller has made sure that the rows behind a sequence are
- * its own.  In range: seq_len >= 0, seq_len + n_path <= seq_cap, rows inside
- * the cache; a sequence out of range keeps new_len = seq_len.  With N = 1 and
- * path 0 this appends one new token to every sequence.
+ * seq_len + j, and new_len[b] (device int32 [B]) = seq_len + n_path.  seq_cap:
+ * device int32 [B], the most rows each sequence may have, or NULL: the caller
+ * has made sure that the rows behind a sequence are its own.  In range:
+ * seq_len >= 0, seq_len + n_path <= seq_cap, rows inside the cache; a sequence
+ * out of range keeps new_len = seq_len.  With N = 1 and path 0 this appends one
+ * new token to every sequence.
  *
  * yoco_swa_tree_commit: node path[j]'s K / V go to ring slot p mod window, p =
  * node_pos[b][path[j]], and slot_pos there becomes p; of entries that share a

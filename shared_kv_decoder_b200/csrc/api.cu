@@ -23,6 +23,10 @@ namespace {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool ok_ptr(const void *p) { return p != nullptr && aligned16(p); }
+bool overlap(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
+}
 bool ok_opt(const void *p) { return p == nullptr || aligned16(p); }
 // The decode kernels address cache rows with 32-bit TMA coordinates.
 bool ok_cache_rows(int64_t rows) { return rows >= 1 && rows <= INT32_MAX; }
@@ -525,11 +529,17 @@ yoco_status yoco_cross_tree_commit(const void *k_nodes, const void *v_nodes, con
                                    cudaStream_t stream) {
     yoco_status st = check_cfg(cfg);
     if (st != YOCO_OK) return st;
-    if (B < 0 || N < 1 || !ok_cache_rows(cache_rows) || (new_len && new_len == seq_len)) return YOCO_ERR_INVALID;
+    if (B < 0 || N < 1 || !ok_cache_rows(cache_rows)) return YOCO_ERR_INVALID;
     if (N > kTreeMaxNodes) return YOCO_ERR_UNSUPPORTED;
     if (B == 0) return YOCO_OK;
     if (!ok_ptr(k_nodes) || !ok_ptr(v_nodes) || !ok_ptr(path) || !ok_ptr(n_path) || !ok_ptr(k_cache) ||
         !ok_ptr(v_cache) || !ok_ptr(seq_start) || !ok_ptr(seq_len) || !ok_opt(seq_cap) || !ok_ptr(new_len))
+        return YOCO_ERR_INVALID;
+    // other CTAs of a sequence read these while the first one writes new_len
+    const int64_t per_seq = 4 * (int64_t)B;
+    if (overlap(new_len, per_seq, seq_len, per_seq) || overlap(new_len, per_seq, n_path, per_seq) ||
+        overlap(new_len, per_seq, seq_cap, per_seq) || overlap(new_len, per_seq, seq_start, 2 * per_seq) ||
+        overlap(new_len, per_seq, path, per_seq * N))
         return YOCO_ERR_INVALID;
     CommitArgs a;
     a.k_nodes = k_nodes; a.v_nodes = v_nodes; a.path = path; a.n_path = n_path; a.B = B; a.N = N;
@@ -551,6 +561,10 @@ yoco_status yoco_swa_tree_commit(const void *k_nodes, const void *v_nodes, const
     if (B == 0) return YOCO_OK;
     if (!ok_ptr(k_nodes) || !ok_ptr(v_nodes) || !ok_ptr(node_pos) || !ok_ptr(path) || !ok_ptr(n_path) ||
         !ok_ptr(ring_k) || !ok_ptr(ring_v) || !ok_ptr(slot_pos))
+        return YOCO_ERR_INVALID;
+    const int64_t per_seq = 4 * (int64_t)B, slots = per_seq * window;   // as above
+    if (overlap(slot_pos, slots, n_path, per_seq) || overlap(slot_pos, slots, path, per_seq * N) ||
+        overlap(slot_pos, slots, node_pos, 2 * per_seq * N))
         return YOCO_ERR_INVALID;
     CommitArgs a;
     a.k_nodes = k_nodes; a.v_nodes = v_nodes; a.path = path; a.n_path = n_path; a.B = B; a.N = N;

@@ -620,6 +620,7 @@ cudaError_t launch_d(const TreeArgs &a, const TreePlan &pl, cudaStream_t st) {
 
 bool make_tree_plan(int32_t B, int32_t N, int64_t max_len, int Hq, int Hkv, int D, int dtype, TreePlan *plan) {
     TreePlan pl;
+    if ((int64_t)B * N > (int64_t)INT32_MAX / 2 / Hq) return false;
     // bf16: the tensor-core kernel, one row tile of 128 or two; fp32: CUDA cores, in
     // row blocks of 8, 16, 32, 64 or 128 (what they take: at the kernels)
     const int R = N * (Hq / Hkv);
@@ -653,7 +654,7 @@ bool make_tree_plan(int32_t B, int32_t N, int64_t max_len, int Hq, int Hkv, int 
     // tiles at full length: no group without a tile is launched
     const int64_t blocks = (int64_t)B * n_rt * (Hkv / pl.heads);
     const int64_t tiles = blocks * stream_tiles;
-    if ((int64_t)B * N * Hq > (int64_t)INT32_MAX / 2 || tiles > INT32_MAX / 2) return false;
+    if (tiles > INT32_MAX / 2) return false;
     pl.groups = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, sms / pl.heads));
     pl.ml_off = ((size_t)(B + 2) * sizeof(int32_t) + 15) / 16 * 16;
     const size_t entries = (size_t)pl.groups * pl.heads * 2 * pl.rows;

@@ -140,6 +140,37 @@ def test_commit_arguments_rejected_before_launch():
     assert swa(b=0) == yoco.OK
 
 
+def test_commit_outputs_apart_from_what_it_reads():
+    L = yoco.load()
+    B, N, W = 64, 8, 32
+    at = lambda base, byte: ctypes.c_void_p(base.value + byte)
+    far = [ctypes.c_void_p(0x1000000 * i) for i in range(1, 9)]
+
+    def cross(nl, cap=far[4]):
+        return L.yoco_cross_tree_commit(FAKE, FAKE, far[0], far[1], B, N, FAKE, FAKE, 100, far[2], far[3], cap, nl, _cfg(),
+                                        None)
+    for x, size in [(far[0], 4 * B * N), (far[1], 4 * B), (far[2], 8 * B), (far[3], 4 * B), (far[4], 4 * B)]:
+        for byte in (0, size - 16, 16 - 4 * B):
+            assert cross(at(x, byte)) == yoco.ERR_INVALID
+
+    def swa(sp):
+        return L.yoco_swa_tree_commit(FAKE, FAKE, far[2], far[0], far[1], B, N, W, FAKE, FAKE, sp, _cfg(), None)
+    for x, size in [(far[0], 4 * B * N), (far[1], 4 * B), (far[2], 8 * B * N)]:
+        for byte in (0, size - 16, 16 - 4 * B * W):
+            assert swa(at(x, byte)) == yoco.ERR_INVALID
+
+
+def test_sizes_beyond_any_tensor():
+    L = yoco.load()
+    big = 2 ** 31 - 1
+    for dtype in (0, 1):
+        for B, N, Hq in [(big, 64, big), (big, 2, 4), (big, 64, 8)]:
+            cfg = _cfg(Hq=Hq, Hkv=Hq, dtype=dtype)
+            assert L.yoco_cross_decode_tree_workspace_size(B, N, big, cfg) == 0
+            assert L.yoco_cross_decode_tree(FAKE, FAKE, FAKE, FAKE, FAKE, 100, FAKE, FAKE, None, None, B, N, big, FAKE, None,
+                                            FAKE, 1 << 60, cfg, None) == yoco.ERR_UNSUPPORTED
+
+
 def test_workspace_sizes():
     sizes = [yoco.cross_decode_tree_workspace_size(B, N, M, 32, 8, 128, torch.bfloat16)
              for B, N, M in [(32, 1, 64), (1, 1, 131072), (4, 16, 65536), (16, 64, 131072)]]
