@@ -105,6 +105,7 @@ cudaError_t launch_commit(const CommitArgs &a, cudaStream_t st) {
     // parts: enough for every chunk of a full path to be in flight at once, no
     // more CTAs than a few waves
     const int64_t chunks = (int64_t)a.N * (a.row_bytes / 16);
+    if (chunks > INT32_MAX / 2) return cudaErrorNotSupported;   // counted in 32 bits
     const int64_t parts = (chunks + kCommitThreads * kUnroll - 1) / (kCommitThreads * kUnroll);
     const int64_t room = std::max<int64_t>(1, (int64_t)4 * device_sm_count() / std::max(1, a.B));
     const dim3 grid((unsigned)a.B, 2, (unsigned)std::max<int64_t>(1, std::min(parts, room)));

@@ -169,6 +169,14 @@ def test_sizes_beyond_any_tensor():
             assert L.yoco_cross_decode_tree_workspace_size(B, N, big, cfg) == 0
             assert L.yoco_cross_decode_tree(FAKE, FAKE, FAKE, FAKE, FAKE, 100, FAKE, FAKE, None, None, B, N, big, FAKE, None,
                                             FAKE, 1 << 60, cfg, None) == yoco.ERR_UNSUPPORTED
+        cfg = _cfg(Hq=big, Hkv=big, dtype=dtype)
+        far = [ctypes.c_void_p(0x1000000 * i) for i in range(1, 6)]
+        assert L.yoco_rope(FAKE, FAKE, 1, 1, None, 0, 0, FAKE, FAKE, ctypes.byref(yoco.rope_config(64)), cfg,
+                           None) == yoco.ERR_UNSUPPORTED
+        assert L.yoco_cross_tree_commit(FAKE, FAKE, far[0], far[1], 1, 64, FAKE, FAKE, 100, far[2], far[3], None, far[4],
+                                        cfg, None) == yoco.ERR_UNSUPPORTED
+        assert L.yoco_swa_tree_commit(FAKE, FAKE, far[2], far[0], far[1], 1, 64, 8, FAKE, FAKE, far[3], cfg,
+                                      None) == yoco.ERR_UNSUPPORTED
 
 
 def test_workspace_sizes():
