@@ -101,7 +101,9 @@ YOCO_DEV void load_rows(const Params &p, const Seg &g, int rows, float *sq, uint
         const int i = (g.rt * RS + (int)threadIdx.x) >> p.lg;
         const bool there = (int)threadIdx.x < rows;
         s_nodes[threadIdx.x] = there ? visible_nodes<RING>(p, g.b, g.n, i) : 0;
-        if (RING) s_bounds[threadIdx.x] = there ? ring_bounds(p.node_pos[(int64_t)g.b * p.N + i], p.window) : RingBounds{-1, -1};
+        if (RING)
+            s_bounds[threadIdx.x] =
+                there ? ring_bounds(p.node_pos[(int64_t)g.b * p.N + i], p.window) : RingBounds{-1, -1};
     }
 }
 
@@ -112,9 +114,10 @@ YOCO_DEV void store_four(const Params &p, const Seg &g, int r, int col4, float m
     if (g.whole) {
         const bool none = m == -INFINITY && L == 0.f;   // a NaN sum is not nothing
         const float inv = none ? 0.f : 1.f / L;
-        *reinterpret_cast<float4 *>(static_cast<float *>(p.o) + (((int64_t)g.b * p.N + node) * p.Hq + h) * D + 4 * col4) =
-            make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-        if (p.lse && col4 == 0) p.lse[((int64_t)g.b * p.Hq + h) * p.N + node] = none ? -INFINITY : (m + log2f(L)) * kLn2;
+        float *dst = static_cast<float *>(p.o) + (((int64_t)g.b * p.N + node) * p.Hq + h) * D;
+        *reinterpret_cast<float4 *>(dst + 4 * col4) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+        if (p.lse && col4 == 0)
+            p.lse[((int64_t)g.b * p.Hq + h) * p.N + node] = none ? -INFINITY : (m + log2f(L)) * kLn2;
     } else {
         const int64_t e = (int64_t)blockIdx.x * 2 + g.slot;
         if (col4 == 0) p.ws_ml[e * RS + r] = make_float2(m, L);
@@ -170,7 +173,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) tree_few_kernel(const __grid_c
     while (it.next(p, g)) {
         const int rows = min(RS, (g.n << p.lg) - g.rt * RS);
         for (int i = 0; i < kFewStages - 1; ++i) {
-            if (g.t0 + i < g.t1) load_tile<D, RING, kFewThreads, PITCH, true, true>(p, g, g.t0 + i, Stage<PITCH>(stages, s_slot, i));
+            if (g.t0 + i < g.t1)
+                load_tile<D, RING, kFewThreads, PITCH, true, true>(p, g, g.t0 + i, Stage<PITCH>(stages, s_slot, i));
             else asm volatile("cp.async.commit_group;" ::: "memory");
         }
         load_rows<D, RING, RS, kFewThreads, PITCH>(p, g, rows, sq, s_nodes, s_bounds);
@@ -355,7 +359,8 @@ __global__ void __launch_bounds__(kRowThreads, 1) tree_simt_kernel(const __grid_
 #pragma unroll
                 for (int i = 0; i < RT; ++i) a[i] = *reinterpret_cast<const float4 *>(sq + (ty + 16 * i) * PITCH + d);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) bk[j] = *reinterpret_cast<const float4 *>(cur.k + (tx + 16 * j) * PITCH + d);
+                for (int j = 0; j < 4; ++j)
+                    bk[j] = *reinterpret_cast<const float4 *>(cur.k + (tx + 16 * j) * PITCH + d);
 #pragma unroll
                 for (int i = 0; i < RT; ++i)
 #pragma unroll
@@ -413,7 +418,8 @@ __global__ void __launch_bounds__(kRowThreads, 1) tree_simt_kernel(const __grid_
                     for (int u = 0; u < 4; ++u)
 #pragma unroll
                         for (int j = 0; j < NJ; ++j) {
-                            const float4 v = *reinterpret_cast<const float4 *>(cur.v + (c + u) * PITCH + 4 * tx + 64 * j);
+                            const float4 v =
+                                *reinterpret_cast<const float4 *>(cur.v + (c + u) * PITCH + 4 * tx + 64 * j);
 #pragma unroll
                             for (int i = 0; i < RT; ++i) {
                                 o[i][4 * j] = fmaf(w[i][u], v.x, o[i][4 * j]);
@@ -464,7 +470,8 @@ __global__ void __launch_bounds__(kRowThreads, 1) tree_simt_kernel(const __grid_
 // share grid.y + 1 starts inside of (the first of its shares to do so); grid.z:
 // the head in its block.
 template <typename T, int D, bool RING, int RS, int BN, int COLS>
-__global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const __grid_constant__ Params p, const int by_stream) {
+__global__ void __launch_bounds__(32 * kMergeWarps)
+    tree_merge_kernel(const __grid_constant__ Params p, const int by_stream) {
     constexpr int GROUPS = D / 4, AHEAD = 4, COL_BLOCKS = GROUPS / (COLS * kMergeWarps);
     const int lane = threadIdx.x & 31;
     const int sub = (int)blockIdx.x % COL_BLOCKS * COLS * kMergeWarps + (threadIdx.x >> 5);   // the first group
@@ -576,7 +583,8 @@ cudaError_t launch_fp32(const TreeArgs &a, const TreePlan &pl, cudaStream_t st) 
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     note_launches(1);
-    return launch_pdl(kern, dim3(pl.heads * pl.groups), dim3(few ? kFewThreads : kRowThreads), smem, st, make_params(a, pl));
+    return launch_pdl(kern, dim3(pl.heads * pl.groups), dim3(few ? kFewThreads : kRowThreads), smem, st,
+                      make_params(a, pl));
 }
 
 template <typename T, int D, bool RING, int RS, int BN>
@@ -639,7 +647,8 @@ bool make_tree_plan(int32_t B, int32_t N, int64_t max_len, int Hq, int Hkv, int 
     if (dtype == kBF16)
         for (int i = 0; i < 3; ++i)
             if (const int64_t streams = (int64_t)B * n_rt * Hkv, c = 2 << i;
-                streams <= room[i] && stream_tiles <= c * (streams * c * 2 >= sms ? tree::kClusterTiles : tree::kFewClusterTiles))
+                streams <= room[i] &&
+                stream_tiles <= c * (streams * c * 2 >= sms ? tree::kClusterTiles : tree::kFewClusterTiles))
                 pl.cluster = (int)c;
     if (pl.cluster) {
         pl.heads = pl.groups = 1;

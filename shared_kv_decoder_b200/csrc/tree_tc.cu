@@ -72,6 +72,9 @@ namespace {
 
 constexpr int BN = kTcKeys;
 constexpr int kThreads = 384;
+// Registers of a thread: at the launch, of a warp that copies or issues, of a softmax warp.
+constexpr int kRegs = 168, kFewRegs = 72, kManyRegs = 216;
+static_assert(128 * kFewRegs + 256 * kManyRegs <= kThreads * kRegs, "no more than the launch has");
 constexpr int kTmemCols = 512;
 constexpr uint32_t kBlk = 128 * 128;   // one [128 rows x 128 bytes] swizzled block
 
@@ -308,176 +311,188 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = misc->tmem;
-    Iter it = [&] {
+    auto segments = [&] {
         if constexpr (CLUSTER) return misc->share;
         else return Iter(p, misc->range);
-    }();
-    Seg sg;
+    };
 
-    if (warp == 8 || warp == 10) {
-        // ----------------------------------------------------- TMA producers
-        const bool one = warp == 8;                     // K / chain A
-        const int ST = one ? L::KST : L::VST;
-        uint64_t *full = &bars[one ? kKFull : kVFull], *empty = &bars[one ? kKEmpty : kVEmpty];
-        int u = 0, k = 0;   // copies, segments whose Q is on its way
-        if (lane == 0) {
-            const bool has_q = PAIR ? !one : one;
-            const uint32_t dst0 = base + (one ? L::K : L::V);
-            bool ok = true;
-            while (ok && !*abort_flag && it.next(p, sg)) {
-                if (has_q) {
-                    for (int hh = 0; hh < L::QTILES && ok; ++hh) {
-                        ok = wait1(&bars[kQEmpty + hh], (k & 1) ^ 1);
-                        if (!ok) break;
-                        mbar_arrive_expect_tx(&bars[kQFull + hh], 128 * D * 2);
-                        const int node0 = (sg.rt * L::QTILES + hh) * (128 >> p.lg);
-                        for (int kb = 0; kb < KB; ++kb)
-                            tc::tma_load_4d(base + L::Q + hh * L::TILE + kb * kBlk, &tm_q, kb * 64, sg.g << p.lg, node0,
-                                            sg.b, &bars[kQFull + hh]);
+    // registers: 384 x 168 at the launch, 128 x 72 + 256 x 216 from here (with 168 for
+    // all, 131 us for the 120 of 64 x 48 nodes over the 1024 ring, 184 for the 177 of
+    // 64 nodes over 131007 tokens)
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+        if (warp == 8 || warp == 10) {
+            // ----------------------------------------------------- TMA producers
+            Iter it = segments();
+            Seg sg;
+            const bool one = warp == 8;                     // K / chain A
+            const int ST = one ? L::KST : L::VST;
+            uint64_t *full = &bars[one ? kKFull : kVFull], *empty = &bars[one ? kKEmpty : kVEmpty];
+            int u = 0, k = 0;   // copies, segments whose Q is on its way
+            if (lane == 0) {
+                const bool has_q = PAIR ? !one : one;
+                const uint32_t dst0 = base + (one ? L::K : L::V);
+                bool ok = true;
+                while (ok && !*abort_flag && it.next(p, sg)) {
+                    if (has_q) {
+                        for (int hh = 0; hh < L::QTILES && ok; ++hh) {
+                            ok = wait1(&bars[kQEmpty + hh], (k & 1) ^ 1);
+                            if (!ok) break;
+                            mbar_arrive_expect_tx(&bars[kQFull + hh], 128 * D * 2);
+                            const int node0 = (sg.rt * L::QTILES + hh) * (128 >> p.lg);
+                            for (int kb = 0; kb < KB; ++kb)
+                                tc::tma_load_4d(base + L::Q + hh * L::TILE + kb * kBlk, &tm_q, kb * 64, sg.g << p.lg, node0,
+                                                sg.b, &bars[kQFull + hh]);
+                        }
+                        if (ok) ++k;
                     }
-                    if (ok) ++k;
-                }
-                for (int t = sg.t0 + (PAIR || one ? 0 : 1); ok && t < sg.t1; t += PAIR ? 1 : 2) {
-                    const bool nodes = t == sg.n_ctx_tiles;
-                    const int row = nodes ? 0 : RING ? t * BN : (int)(sg.row0 + (int64_t)t * BN);
-                    const int b = nodes || RING ? sg.b : 0;
-#pragma unroll
-                    for (int e = 0; e < (PAIR ? 1 : 2) && ok; ++e) {
-                        const bool is_k = PAIR ? one : e == 0;
-                        const CUtensorMap *map = is_k ? nodes ? &tm_kn : &tm_k : nodes ? &tm_vn : &tm_v;
-                        const int st = u % ST;
-                        ok = wait1(&empty[st], ((u / ST) & 1) ^ 1);
-                        if (!ok) break;
-                        mbar_arrive_expect_tx(&full[st], (nodes ? kTreeMaxNodes : BN) * D * 2);
-                        for (int kb = 0; kb < KB; ++kb)
-                            tc::tma_load_4d(dst0 + st * L::TILE + kb * kBlk, map, kb * 64, sg.g, row, b, &full[st]);
-                        ++u;
+                    for (int t = sg.t0 + (PAIR || one ? 0 : 1); ok && t < sg.t1; t += PAIR ? 1 : 2) {
+                        const bool nodes = t == sg.n_ctx_tiles;
+                        const int row = nodes ? 0 : RING ? t * BN : (int)(sg.row0 + (int64_t)t * BN);
+                        const int b = nodes || RING ? sg.b : 0;
+    #pragma unroll
+                        for (int e = 0; e < (PAIR ? 1 : 2) && ok; ++e) {
+                            const bool is_k = PAIR ? one : e == 0;
+                            const CUtensorMap *map = is_k ? nodes ? &tm_kn : &tm_k : nodes ? &tm_vn : &tm_v;
+                            const int st = u % ST;
+                            ok = wait1(&empty[st], ((u / ST) & 1) ^ 1);
+                            if (!ok) break;
+                            mbar_arrive_expect_tx(&full[st], (nodes ? kTreeMaxNodes : BN) * D * 2);
+                            for (int kb = 0; kb < KB; ++kb)
+                                tc::tma_load_4d(dst0 + st * L::TILE + kb * kBlk, map, kb * 64, sg.g, row, b, &full[st]);
+                            ++u;
+                        }
                     }
                 }
+                if (!ok) *abort_flag = 1;
             }
-            if (!ok) *abort_flag = 1;
-        }
-        __syncwarp();
-        // with every copy issued, these warps have time
-        if (!CLUSTER) fill_rows_without_node<__nv_bfloat16, D, RING, RS, BN>(p, warp == 10, 2, &g_status_tree_tc);
-        if (lane == 0) {
-            // drain: the last copies issued must land before this CTA may exit
-            for (int q = max(0, u - ST); q < u; ++q)
-                if (!wait1(&full[q % ST], (q / ST) & 1)) break;
-            if (k > 0)
-                for (int hh = 0; hh < L::QTILES; ++hh)
-                    if (!wait1(&bars[kQFull + hh], (k - 1) & 1)) break;
-        }
-    } else if (warp == 9 || warp == 11) {
-        // ------------------------------------------- MMA issue of one chain
-        if (lane == 0) {
-            const int hh = warp == 9 ? 0 : 1;
-            constexpr uint32_t idS = tc::idesc_bf16(128, BN, false, false);
-            constexpr uint32_t idPV = tc::idesc_bf16(128, D, false, true);
-            // descriptors as (low, high) words: the low one holds the address and the
-            // leading offset, so a step is one 32-bit addition
-            constexpr uint32_t kHi = (1024u >> 4) | 1u << 14 | 2u << 29;
-            constexpr uint32_t kLoS = (16u >> 4) << 16, kLoV = (kBlk >> 4) << 16;
-            // (a CTA of a cluster has its rank in the bits above its shared-memory offsets)
-            const uint32_t off0 = base & 0x3ffffu;
-            const uint32_t q_lo = ((off0 + L::Q + (PAIR ? hh * L::TILE : 0)) >> 4) | kLoS;
-            const uint32_t ts = tmem + hh * 128, to = tmem + 256 + hh * 128;
-            auto desc = [](uint32_t lo) { return (uint64_t)kHi << 32 | lo; };
-            uint64_t *q_full = &bars[kQFull + (PAIR ? hh : 0)], *q_empty = &bars[kQEmpty + (PAIR ? hh : 0)];
-            // PAIR: the K stages and the V stages, both chains'.  ALT: the chain's one
-            // ring in both roles
-            struct Ring {
-                uint64_t *full, *empty;
-                uint32_t addr, phase;
-                int st, n;
-                YOCO_DEV void advance() {
-                    if (++st == n) {
-                        st = 0;
-                        phase ^= 1;
+            __syncwarp();
+            // with every copy issued, these warps have time
+            if (!CLUSTER) fill_rows_without_node<__nv_bfloat16, D, RING, RS, BN>(p, warp == 10, 2, &g_status_tree_tc);
+            if (lane == 0) {
+                // drain: the last copies issued must land before this CTA may exit
+                for (int q = max(0, u - ST); q < u; ++q)
+                    if (!wait1(&full[q % ST], (q / ST) & 1)) break;
+                if (k > 0)
+                    for (int hh = 0; hh < L::QTILES; ++hh)
+                        if (!wait1(&bars[kQFull + hh], (k - 1) & 1)) break;
+            }
+        } else {
+            // ------------------------------------------- MMA issue of one chain
+            if (lane == 0) {
+                Iter it = segments();
+                Seg sg;
+                const int hh = warp == 9 ? 0 : 1;
+                constexpr uint32_t idS = tc::idesc_bf16(128, BN, false, false);
+                constexpr uint32_t idPV = tc::idesc_bf16(128, D, false, true);
+                // descriptors as (low, high) words: the low one holds the address and the
+                // leading offset, so a step is one 32-bit addition
+                constexpr uint32_t kHi = (1024u >> 4) | 1u << 14 | 2u << 29;
+                constexpr uint32_t kLoS = (16u >> 4) << 16, kLoV = (kBlk >> 4) << 16;
+                // (a CTA of a cluster has its rank in the bits above its shared-memory offsets)
+                const uint32_t off0 = base & 0x3ffffu;
+                const uint32_t q_lo = ((off0 + L::Q + (PAIR ? hh * L::TILE : 0)) >> 4) | kLoS;
+                const uint32_t ts = tmem + hh * 128, to = tmem + 256 + hh * 128;
+                auto desc = [](uint32_t lo) { return (uint64_t)kHi << 32 | lo; };
+                uint64_t *q_full = &bars[kQFull + (PAIR ? hh : 0)], *q_empty = &bars[kQEmpty + (PAIR ? hh : 0)];
+                // PAIR: the K stages and the V stages, both chains'.  ALT: the chain's one
+                // ring in both roles
+                struct Ring {
+                    uint64_t *full, *empty;
+                    uint32_t addr, phase;
+                    int st, n;
+                    YOCO_DEV void advance() {
+                        if (++st == n) {
+                            st = 0;
+                            phase ^= 1;
+                        }
                     }
-                }
-            };
-            const bool one = PAIR || hh == 0;
-            Ring rk = {&bars[one ? kKFull : kVFull], &bars[one ? kKEmpty : kVEmpty], (off0 + (one ? L::K : L::V)) >> 4, 0,
-                       0, L::KST};
-            Ring rv_own = {&bars[kVFull], &bars[kVEmpty], (off0 + L::V) >> 4, 0, 0, L::VST};
-            Ring &rv = PAIR ? rv_own : rk;
-            bool ok = true;
-            int seg = 0;
-            uint32_t g = 0, k = 0, turn = 0;   // the chain's tiles, segments and turns
-            for (; ok && !*abort_flag && it.next(p, sg); ++seg) {
-                const int nt = sg.t1 - sg.t0;
-                // tiles of this chain and of chain B; the node tile, if this chain has it
-                const int mine = PAIR ? nt : (nt + 1 - hh) / 2, others_b = PAIR ? nt : nt / 2;
-                const int n_ctx = sg.n_ctx_tiles - sg.t0;
-                const int n_nodes = PAIR ? n_ctx : (n_ctx & 1) == hh ? n_ctx >> 1 : -1;
-                ok = wait1(q_full, seg & 1);
-                if (!ok) break;
-                if (mine == 0) {   // nothing for this chain, which has its say on Q all the same
-                    mbar_arrive(q_empty);
-                    continue;
-                }
-                // step n: P V of tile n - 1 and S of tile n, the chains in turns (A's step
-                // 0, B's step 0, A's step 1, ...), so that one chain's MMAs run under the
-                // other's softmax: unordered, the two fall into step, with the exponentials
-                // of both at once and then the MMAs of both at once
-                for (int n = 0; n <= mine; ++n) {
-                    uint32_t vd = 0;
-                    uint64_t *v_empty = nullptr;
-                    if (n > 0) {
-                        ok = wait1(&rv.full[rv.st], rv.phase) &&
-                             (!PAIR || hh == 0 || wait1(&bars[kVClean + rv.st], rv.phase)) &&
-                             (n > 1 || k == 0 || wait1(&bars[kOFree + hh], (k - 1) & 1));
-                        vd = (rv.addr + rv.st * (L::TILE >> 4)) | kLoV;
-                        v_empty = &rv.empty[rv.st];
-                        rv.advance();
-                    }
-                    ok = ok && (n == mine || wait1(&rk.full[rk.st], rk.phase));
-                    if (n > 0) ok = ok && wait1(&bars[kPFull + hh], g++ & 1);
-                    if (hh == 1 || (others_b > 0 && n > 0)) ok = ok && wait1(&bars[kTurn + hh], turn++ & 1);
+                };
+                const bool one = PAIR || hh == 0;
+                Ring rk = {&bars[one ? kKFull : kVFull], &bars[one ? kKEmpty : kVEmpty], (off0 + (one ? L::K : L::V)) >> 4, 0,
+                           0, L::KST};
+                Ring rv_own = {&bars[kVFull], &bars[kVEmpty], (off0 + L::V) >> 4, 0, 0, L::VST};
+                Ring &rv = PAIR ? rv_own : rk;
+                bool ok = true;
+                int seg = 0;
+                uint32_t g = 0, k = 0, turn = 0;   // the chain's tiles, segments and turns
+                for (; ok && !*abort_flag && it.next(p, sg); ++seg) {
+                    const int nt = sg.t1 - sg.t0;
+                    // tiles of this chain and of chain B; the node tile, if this chain has it
+                    const int mine = PAIR ? nt : (nt + 1 - hh) / 2, others_b = PAIR ? nt : nt / 2;
+                    const int n_ctx = sg.n_ctx_tiles - sg.t0;
+                    const int n_nodes = PAIR ? n_ctx : (n_ctx & 1) == hh ? n_ctx >> 1 : -1;
+                    ok = wait1(q_full, seg & 1);
                     if (!ok) break;
-                    tc::fence_after_sync();
-                    if (n > 0) {
-                        tc::mma_bf16_ts(to, ts, desc(vd), idPV, n > 1 ? 1u : 0u);
-#pragma unroll
-                        for (int kk = 1; kk < kTreeMaxNodes / 16; ++kk)
-                            tc::mma_bf16_ts(to, ts + kk * 8, desc(vd + kk * (2048 >> 4)), idPV, 1u);
-                        if (n - 1 != n_nodes) {
-#pragma unroll
-                            for (int kk = kTreeMaxNodes / 16; kk < BN / 16; ++kk)
+                    if (mine == 0) {   // nothing for this chain, which has its say on Q all the same
+                        mbar_arrive(q_empty);
+                        continue;
+                    }
+                    // step n: P V of tile n - 1 and S of tile n, the chains in turns (A's step
+                    // 0, B's step 0, A's step 1, ...), so that one chain's MMAs run under the
+                    // other's softmax: unordered, the two fall into step, with the exponentials
+                    // of both at once and then the MMAs of both at once
+                    for (int n = 0; n <= mine; ++n) {
+                        uint32_t vd = 0;
+                        uint64_t *v_empty = nullptr;
+                        if (n > 0) {
+                            ok = wait1(&rv.full[rv.st], rv.phase) &&
+                                 (!PAIR || hh == 0 || wait1(&bars[kVClean + rv.st], rv.phase)) &&
+                                 (n > 1 || k == 0 || wait1(&bars[kOFree + hh], (k - 1) & 1));
+                            vd = (rv.addr + rv.st * (L::TILE >> 4)) | kLoV;
+                            v_empty = &rv.empty[rv.st];
+                            rv.advance();
+                        }
+                        ok = ok && (n == mine || wait1(&rk.full[rk.st], rk.phase));
+                        if (n > 0) ok = ok && wait1(&bars[kPFull + hh], g++ & 1);
+                        if (hh == 1 || (others_b > 0 && n > 0)) ok = ok && wait1(&bars[kTurn + hh], turn++ & 1);
+                        if (!ok) break;
+                        tc::fence_after_sync();
+                        if (n > 0) {
+                            tc::mma_bf16_ts(to, ts, desc(vd), idPV, n > 1 ? 1u : 0u);
+    #pragma unroll
+                            for (int kk = 1; kk < kTreeMaxNodes / 16; ++kk)
                                 tc::mma_bf16_ts(to, ts + kk * 8, desc(vd + kk * (2048 >> 4)), idPV, 1u);
+                            if (n - 1 != n_nodes) {
+    #pragma unroll
+                                for (int kk = kTreeMaxNodes / 16; kk < BN / 16; ++kk)
+                                    tc::mma_bf16_ts(to, ts + kk * 8, desc(vd + kk * (2048 >> 4)), idPV, 1u);
+                            }
+                            tc::mma_commit(v_empty);
                         }
-                        tc::mma_commit(v_empty);
-                    }
-                    if (n < mine) {
-                        const uint32_t kd = (rk.addr + rk.st * (L::TILE >> 4)) | kLoS;
-#pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint32_t off = ((kk >> 2) * kBlk + (kk & 3) * 32) >> 4;
-                            tc::mma_bf16_ss(ts, desc(q_lo + off), desc(kd + off), idS, kk > 0 ? 1u : 0u);
+                        if (n < mine) {
+                            const uint32_t kd = (rk.addr + rk.st * (L::TILE >> 4)) | kLoS;
+    #pragma unroll
+                            for (int kk = 0; kk < D / 16; ++kk) {
+                                const uint32_t off = ((kk >> 2) * kBlk + (kk & 3) * 32) >> 4;
+                                tc::mma_bf16_ss(ts, desc(q_lo + off), desc(kd + off), idS, kk > 0 ? 1u : 0u);
+                            }
                         }
+                        if (hh == 1 || n <= others_b - (others_b == 0)) mbar_arrive(&bars[kTurn + (hh ^ 1)]);
+                        if (n < mine) {
+                            tc::mma_commit(&bars[kSFull + hh]);
+                            tc::mma_commit(&rk.empty[rk.st]);
+                            rk.advance();
+                            if (n == mine - 1) tc::mma_commit(q_empty);
+                        }
+                        if (n > 0) tc::mma_commit(&bars[kODone + hh]);
                     }
-                    if (hh == 1 || n <= others_b - (others_b == 0)) mbar_arrive(&bars[kTurn + (hh ^ 1)]);
-                    if (n < mine) {
-                        tc::mma_commit(&bars[kSFull + hh]);
-                        tc::mma_commit(&rk.empty[rk.st]);
-                        rk.advance();
-                        if (n == mine - 1) tc::mma_commit(q_empty);
-                    }
-                    if (n > 0) tc::mma_commit(&bars[kODone + hh]);
+                    if (!ok) break;
+                    // as many of chain B's turns behind chain A as it has steps
+                    if (hh == 0 && others_b == mine) ok = wait1(&bars[kTurn], turn++ & 1);
+                    ++k;
                 }
-                if (!ok) break;
-                // as many of chain B's turns behind chain A as it has steps
-                if (hh == 0 && others_b == mine) ok = wait1(&bars[kTurn], turn++ & 1);
-                ++k;
+                if (!ok) *abort_flag = 1;
+                // every MMA issued by this thread has finished before TMEM is freed
+                tc::mma_commit(&bars[kDrain + hh]);
+                wait1(&bars[kDrain + hh], 0);
             }
-            if (!ok) *abort_flag = 1;
-            // every MMA issued by this thread has finished before TMEM is freed
-            tc::mma_commit(&bars[kDrain + hh]);
-            wait1(&bars[kDrain + hh], 0);
         }
     } else {
         // ------------------------------------------------------------ softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
+        Iter it = segments();
+        Seg sg;
         const int hh = warp >> 2;
         const int r = threadIdx.x & 127;           // row in tile == TMEM lane
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
@@ -897,6 +912,12 @@ bool make_map(CUtensorMap *m, const void *ptr, int64_t D, int64_t d1, int64_t d2
     return encode_bf16_map_4d(m, ptr, dims, strides, box);
 }
 
+template <typename F>
+bool has_registers(F *kern) {
+    cudaFuncAttributes a;
+    return cudaFuncGetAttributes(&a, kern) == cudaSuccess && a.numRegs >= kRegs;
+}
+
 template <int D, bool RING, bool PAIR>
 cudaError_t launch_tc(const TreeArgs &a, const TreePlan &pl, cudaStream_t st) {
     const int G = a.Hq / a.Hkv;
@@ -910,6 +931,10 @@ cudaError_t launch_tc(const TreeArgs &a, const TreePlan &pl, cudaStream_t st) {
     constexpr size_t smem = Smem<D, PAIR>::ALLOC;
     const bool cl = pl.cluster > 0;
     auto kern = cl ? tree_tc_kernel<D, RING, PAIR, true> : tree_tc_kernel<D, RING, PAIR, false>;
+    // a build with fewer registers than kRegs would wait for the rest for good
+    static const bool regs_ok[2] = {has_registers(tree_tc_kernel<D, RING, PAIR, false>),
+                                    has_registers(tree_tc_kernel<D, RING, PAIR, true>)};
+    if (!regs_ok[cl]) return cudaErrorInvalidDeviceFunction;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     note_launches(1);
