@@ -91,7 +91,7 @@ struct Smem {
     static constexpr uint32_t V = K + KST * TILE;
     static constexpr uint32_t ML = V + VST * TILE;      // float2[128]: chain B's (m, l)
     static constexpr uint32_t BAR = ML + 128 * 8;
-    static constexpr uint32_t MISC = BAR + 48 * 8;
+    static constexpr uint32_t MISC = BAR + 50 * 8;
     static constexpr uint32_t BYTES = MISC + 256;
     static constexpr uint32_t ALLOC = BYTES + 1024;     // alignment slack
 };
@@ -112,7 +112,8 @@ enum Bar {
     kVEmpty = 33,
     kVClean = 39,  // PAIR: chain A is done with cleaning the tile (4 arrivals)
     kTurn = 45,    // 2: chain A's / B's turn to issue MMAs
-    kNumBars = 47
+    kPHalf = 47,   // 2: the first 64 columns of P written (4 arrivals)
+    kNumBars = 49
 };
 
 struct Misc {
@@ -267,6 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bars[kQEmpty + s], PAIR ? 1 : 2);   // ALT: both chains read the one tile
             mbar_init(&bars[kSFull + s], 1);
             mbar_init(&bars[kPFull + s], 4);
+            mbar_init(&bars[kPHalf + s], 4);
             mbar_init(&bars[kODone + s], 1);
             mbar_init(&bars[kOFree + s], 4);
             mbar_init(&bars[kTurn + s], 1);
@@ -350,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const bool nodes = t == sg.n_ctx_tiles;
                         const int row = nodes ? 0 : RING ? t * BN : (int)(sg.row0 + (int64_t)t * BN);
                         const int b = nodes || RING ? sg.b : 0;
-    #pragma unroll
+#pragma unroll
                         for (int e = 0; e < (PAIR ? 1 : 2) && ok; ++e) {
                             const bool is_k = PAIR ? one : e == 0;
                             const CUtensorMap *map = is_k ? nodes ? &tm_kn : &tm_k : nodes ? &tm_vn : &tm_v;
@@ -444,17 +446,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                             rv.advance();
                         }
                         ok = ok && (n == mine || wait1(&rk.full[rk.st], rk.phase));
-                        if (n > 0) ok = ok && wait1(&bars[kPFull + hh], g++ & 1);
                         if (hh == 1 || (others_b > 0 && n > 0)) ok = ok && wait1(&bars[kTurn + hh], turn++ & 1);
+                        if (n > 0) ok = ok && wait1(&bars[kPHalf + hh], g & 1);
                         if (!ok) break;
                         tc::fence_after_sync();
                         if (n > 0) {
+                            // the first 64 keys while the softmax forms the weights of the others
                             tc::mma_bf16_ts(to, ts, desc(vd), idPV, n > 1 ? 1u : 0u);
-    #pragma unroll
+#pragma unroll
                             for (int kk = 1; kk < kTreeMaxNodes / 16; ++kk)
                                 tc::mma_bf16_ts(to, ts + kk * 8, desc(vd + kk * (2048 >> 4)), idPV, 1u);
+                            ok = wait1(&bars[kPFull + hh], g++ & 1);
+                            if (!ok) break;
+                            tc::fence_after_sync();
                             if (n - 1 != n_nodes) {
-    #pragma unroll
+#pragma unroll
                                 for (int kk = kTreeMaxNodes / 16; kk < BN / 16; ++kk)
                                     tc::mma_bf16_ts(to, ts + kk * 8, desc(vd + kk * (2048 >> 4)), idPV, 1u);
                             }
@@ -462,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         if (n < mine) {
                             const uint32_t kd = (rk.addr + rk.st * (L::TILE >> 4)) | kLoS;
-    #pragma unroll
+#pragma unroll
                             for (int kk = 0; kk < D / 16; ++kk) {
                                 const uint32_t off = ((kk >> 2) * kBlk + (kk & 3) * 32) >> 4;
                                 tc::mma_bf16_ss(ts, desc(q_lo + off), desc(kd + off), idS, kk > 0 ? 1u : 0u);
@@ -673,6 +679,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!(mx < INFINITY)) m = NAN;
                     const float neg_m = m == -INFINITY ? 0.f : -m;
                     const uint64_t nm2 = tc::f2_pack(neg_m, neg_m);
+                    if (!first && __any_sync(0xffffffffu, grow)) {
+                        if (!waitw(&bars[kODone + hh], (g[hh] - 1) & 1)) { ok = false; break; }
+                        tc::fence_after_sync();
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            float o[32];
+                            tc::tmem_ld32(tO + c, o);
+                            tc::wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] *= alpha;
+                            tc::tmem_st32(tO + c, o);
+                        }
+                    }
                     uint64_t rs2a = 0, rs2b = 0;
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
@@ -698,25 +717,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                             pk[cc / 2] = tc::pack_bf16x2(e0, e1);
                         }
                         tc::tmem_st32u(tS + half * 32, pk);
+                        if (half == 0) {
+                            tc::wait_st();
+                            tc::fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&bars[kPHalf + hh]);
+                        }
                     }
                     float ra0, ra1, rb0, rb1;
                     tc::f2_unpack(rs2a, ra0, ra1);
                     tc::f2_unpack(rs2b, rb0, rb1);
                     l = l * alpha + ((ra0 + ra1) + (rb0 + rb1));
-                    if (!first && __any_sync(0xffffffffu, grow)) {
-                        if (!waitw(&bars[kODone + hh], (g[hh] - 1) & 1)) { ok = false; break; }
-                        tc::fence_after_sync();
-#pragma unroll
-                        for (int c = 0; c < D; c += 32) {
-                            float o[32];
-                            tc::tmem_ld32(tO + c, o);
-                            tc::wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] *= alpha;
-                            tc::tmem_st32(tO + c, o);
-                        }
-                    }
                     tc::wait_st();
+                } else {
+                    __syncwarp();   // the rows of V that it has cleaned
+                    if (lane == 0) mbar_arrive(&bars[kPHalf + hh]);
                 }
                 first = false;
                 tc::fence_before_sync();
