@@ -14,16 +14,20 @@
 // What bounds it.  With R rows of a KV head a 64 KB K / V tile (D = 128) takes
 // 4 * 128 * max(R, 128) * 128 tensor operations; at the measured rates the cache
 // read is the longer one up to about R = 250.  Measured (graph replays on
-// several GPUs): 16 x 64K-128K tokens, 16 nodes (R = 64): 985-1100 us,
-// 5.8-6.4 TB/s of the cache, the clock at 1.3-1.5 GHz under the power cap;
-// 131007 tokens, 64 nodes (R = 256): 177-183 us, 750-780 TFLOP/s, the chain of
-// one tile's softmax (1950 cycles) and the MMAs that wait for it (2000) the
-// limit, tensor pipe 47% busy; 64 x 48 nodes over the 1024 ring: 132 us, a
+// several GPUs): 16 x 64K-128K tokens, 16 nodes (R = 64): 930-1075 us,
+// 5.9-6.8 TB/s of the cache, the clock at 1.3-1.5 GHz under the power cap;
+// 131007 tokens, 64 nodes (R = 256): 163-167 us, 825-843 TFLOP/s, the chain of
+// one tile's softmax (1850 cycles) and the MMAs that wait for it (about 2000) the
+// limit, tensor pipe half busy; 64 x 48 nodes over the 1024 ring: 113-117 us, a
 // segment's start and end (nine tiles) a quarter of it; in clusters 2047 tokens
-// 11.3 us, 4 x 16 nodes over the ring 13.2, latency throughout.
+// 10.5 us, 4 x 16 nodes over the ring 12.8, latency throughout.
 // Two warps a row, 64 columns each, so that the softmax takes 1200 cycles, were
 // slower all the same (1050 for 1007 us, 155 for 142): the two have to agree on
-// the reference, and the power cap takes the rest.
+// the reference, and the power cap takes the rest.  All exponentials are MUFU's:
+// one pair in eight by a polynomial on the FMA pipe paid while the softmax warps
+// had 168 registers (137 for 162 us on the ring), with 216 it costs 2-3% (120 for
+// 117).  The first 64 weights formed by the old reference, with the maximum in
+// their shadow, were no faster (166 for 166) and slower on the ring (142 for 117).
 //
 // Warp roles (384 threads):
 //   warps 0-3, 4-7  softmax chains A and B: thread r owns row r (TMEM lane r)
@@ -194,39 +198,6 @@ YOCO_DEV float max3_nan(float a, float b, float c) {
     asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
-
-// 2^x for a pair on the FMA pipe, x <= 8 or so: x = n + f with n the nearest
-// integer (by adding 1.5 * 2^23) and f in [-1/2, 1/2] (Cody-Waite reduction),
-// 2^f by the polynomial 1 + f (c1 + f (c2 + f (c3 + f c4))), a minimax fit of the
-// relative error under p(0) = 1 (a linear program over 4001 points: 2.9e-6, mean
-// 3.4e-7), 2^n by adding n to the exponent field.  x is held at -127 at the
-// least, where f = 0, p = 1 and the exponent field comes out as zero: a masked
-// score (-inf) gives exactly 0.
-YOCO_DEV void exp2_pair(float x0, float x1, float &e0, float &e1) {
-    constexpr uint64_t kRound = tc::f2_const(0x4B400000u);  // 1.5 * 2^23
-    constexpr uint64_t kOne = tc::f2_const(0x3F800000u);
-    constexpr uint64_t kC1 = tc::f2_const(0x3F317095u);     // 0.69312412
-    constexpr uint64_t kC2 = tc::f2_const(0x3E7601C1u);     // 0.24024107
-    constexpr uint64_t kC3 = tc::f2_const(0x3D64FE8Fu);     // 0.05590683
-    constexpr uint64_t kC4 = tc::f2_const(0x3C1D003Du);     // 0.00958258
-    const uint64_t X = tc::f2_pack(fmaxf(x0, -127.f), fmaxf(x1, -127.f));
-    const uint64_t T = tc::f2_add(X, kRound);
-    const uint64_t F = tc::f2_sub(X, tc::f2_sub(T, kRound));
-    uint64_t P = tc::f2_fma(F, kC4, kC3);
-    P = tc::f2_fma(P, F, kC2);
-    P = tc::f2_fma(P, F, kC1);
-    P = tc::f2_fma(P, F, kOne);
-    float p0, p1, t0, t1;
-    tc::f2_unpack(P, p0, p1);
-    tc::f2_unpack(T, t0, t1);
-    e0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23));
-    e1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23));
-}
-
-// Of every eight pairs of columns, how many take the FMA pipe.  64 x 48 nodes over
-// the 1024 ring: none 162 us, one 137, two 142, three 146, four 178 (the first and
-// last of an earlier build); the long contexts do not tell one from three.
-constexpr int kPoly = 1;
 
 // A ring segment's bounds over all its nodes: what every node sees and what
 // any does.
@@ -701,13 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const int c = half * (BN / 2) + cc;
                             float x0, x1;
                             tc::f2_unpack(tc::f2_fma(tc::f2_pack(s[c], s[c + 1]), sl2, nm2), x0, x1);
-                            float e0, e1;
-                            if ((c >> 1) * kPoly % 8 < kPoly) {
-                                exp2_pair(x0, x1, e0, e1);
-                            } else {
-                                e0 = tc::ex2(x0);
-                                e1 = tc::ex2(x1);
-                            }
+                            const float e0 = tc::ex2(x0), e1 = tc::ex2(x1);
                             if (c & 2)
                                 rs2b = tc::f2_add(rs2b, tc::f2_pack(e0, e1));
                             else
