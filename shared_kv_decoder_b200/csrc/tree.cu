@@ -127,9 +127,8 @@ YOCO_DEV void store_four(const Params &p, const Seg &g, int r, int col4, float m
 
 }  // namespace
 
-// fp32 on the CUDA cores, up to 32 rows of a KV head: bound by issue slots, for
-// eight rows about as much by the cache read (two tiles are on their way while one
-// computes).  A warp has eight rows and KW keys of every tile, with statistics of
+// fp32 on the CUDA cores, up to 32 rows of a KV head: bound by issue slots
+// (69% taken; two tiles are on their way while one computes).  A warp has eight rows and KW keys of every tile, with statistics of
 // its own, so that nothing is exchanged before the segment ends.  A lane has CPL
 // columns of q, K, V and o: K and V are read from shared memory once, in whole
 // rows, and q stays in registers.  The columns' sums for four keys by eight rows
@@ -137,8 +136,8 @@ YOCO_DEV void store_four(const Params &p, const Seg &g, int r, int col4, float m
 // loaded in an order that puts what it keeps first, so that no exchange has to
 // choose.  A key that a row does not see is left out of the product (its weight is
 // held as -1), so what its K and V hold never reaches the row.
-// Over 8 x 8192 keys of 8 heads, D = 128: 8 rows take 116 us (4.6 TB/s), 16 take
-// 190, 32 take 315 (390 in the kernel below).  With a lane per key and q in shared
+// Over 8 x 8192 keys of 8 heads, D = 128: 8 rows take 118 us (4.5 TB/s), 16 take
+// 192, 32 take 317 (390 in the kernel below).  With a lane per key and q in shared
 // memory, where an operand that all lanes share costs as much as one that they do
 // not, 138, 221 and 368; with exchanges that choose, the same; with pairs of rows in
 // packed FMAs 155, 265 and 462.
