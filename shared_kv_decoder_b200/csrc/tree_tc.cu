@@ -108,7 +108,7 @@ enum Bar {
     kPFull = 6,    // 2: P written (4 arrivals, one a warp)
     kODone = 8,    // 2: P.V finished
     kOFree = 10,   // 2: O read out (4 arrivals)
-    kML = 12,      // chain B's (m, l) written (4 arrivals)
+    kML = 12,      // ALT: chain B's (m, l) written; PAIR in clusters: its last P V seen to finish (4 arrivals)
     kDrain = 13,   // 2
     kKFull = 15,   // up to 6 each; ALT: of chain A's ring
     kKEmpty = 21,
@@ -722,8 +722,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 continue;
             }
             if (!waitw(&bars[kODone + hh], (g[hh] - 1) & 1)) { ok = false; break; }
-            // the partial goes over the tiles in shared memory: nobody reads them any more
-            if (CLUSTER && PAIR && !waitw(&bars[kODone + (hh ^ 1)], (g[hh] - 1) & 1)) { ok = false; break; }
+            if constexpr (CLUSTER && PAIR) {
+                // The partial goes over the tiles in shared memory, which the other chain's P V may
+                // still be reading.  A parity alone does not tell its last P V from the one two
+                // before.  Chain B therefore tells chain A that it has seen its own finish.  For
+                // chain B the parity will do: its last P V was issued behind chain A's last one,
+                // that behind chain A's last S, which was read by then, and an S finishes after the
+                // P V before it.
+                if (hh == 1) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars[kML]);
+                    if (!waitw(&bars[kODone], (g[hh] - 1) & 1)) { ok = false; break; }
+                } else if (!waitw(&bars[kML], k[1] & 1)) {
+                    ok = false;
+                    break;
+                }
+            }
             float wa = 1.f, wb = 0.f;
             const bool join = !PAIR && has_b;
             if (join) {
