@@ -627,7 +627,8 @@ cudaError_t launch_d(const TreeArgs &a, const TreePlan &pl, cudaStream_t st) {
 
 bool make_tree_plan(int32_t B, int32_t N, int64_t max_len, int Hq, int Hkv, int D, int dtype, TreePlan *plan) {
     TreePlan pl;
-    if ((int64_t)B * N > (int64_t)INT32_MAX / 2 / Hq) return false;
+    // the 16-byte chunks of a token's heads (up to 32 each) and the rows are counted in 32 bits
+    if (Hq > 1 << 24 || (int64_t)B * N > (int64_t)INT32_MAX / 2 / Hq) return false;
     // bf16: the tensor-core kernel, one row tile of 128 or two; fp32: CUDA cores, in
     // row blocks of 8, 16, 32, 64 or 128 (what they take: at the kernels)
     const int R = N * (Hq / Hkv);

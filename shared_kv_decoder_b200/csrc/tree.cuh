@@ -284,7 +284,7 @@ YOCO_DEV void fill_rows_without_node(const Params &p, int w, int warps, unsigned
         if (!s.ok && node == 0 && lane == 0) atomicOr(status, kStatusBadSequence);
         if (node < s.n) continue;
         uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(p.o) + (int64_t)i * p.Hq * D);
-        for (int c = lane; c < p.Hq * D * (int)sizeof(T) / 16; c += 32) dst[c] = make_uint4(0, 0, 0, 0);
+        for (int c = lane; c < p.Hq * (D * (int)sizeof(T) / 16); c += 32) dst[c] = make_uint4(0, 0, 0, 0);
         if (p.lse)
             for (int h = lane; h < p.Hq; h += 32) p.lse[((int64_t)b * p.Hq + h) * p.N + node] = -INFINITY;
     }

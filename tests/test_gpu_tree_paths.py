@@ -52,3 +52,15 @@ def test_clusters_of_two_row_tiles(cuda_lib, N, G, D, size, B, L):
     ref = tr.cross_tree(q[some], kn[some], vn[some], kc, vc, [starts[b] for b in some], [lens[b] for b in some],
                         [masks[b] for b in some])
     tr.assert_tree(o[some], lse[some], ref, BF)
+
+
+def test_rows_without_a_node_of_very_many_heads(cuda_lib):
+    """A token of 2^22 fp32 heads of 128 is 2^31 bytes."""
+    Hq, D = 1 << 22, 128
+    q = torch.zeros(1, 1, Hq, D, device="cuda")
+    kn, kc = torch.zeros(1, 1, Hq // 8, D, device="cuda"), torch.zeros(1, Hq // 8, D, device="cuda")
+    o = torch.ones_like(q)
+    o, lse = cuda_lib.cross_decode_tree(q, kn, kn, kc, kc, torch.zeros(1, dtype=torch.int64, device="cuda"),
+                                        torch.zeros(1, dtype=torch.int32, device="cuda"), 0,
+                                        n_nodes=torch.zeros(1, dtype=torch.int32, device="cuda"), want_lse=True, o=o)
+    assert not o.any() and torch.isneginf(lse).all()

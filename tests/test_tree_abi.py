@@ -179,6 +179,20 @@ def test_sizes_beyond_any_tensor():
                                       None) == yoco.ERR_UNSUPPORTED
 
 
+def test_tree_heads_beyond_32_bit_rows():
+    # a row of 2^24 heads is 2^29 16-byte chunks (fp32, D = 128); of eight times as many, 2^32
+    L = yoco.load()
+    for dtype in (0, 1):
+        for Hq, ok in [(1 << 24, True), ((1 << 24) + 8, False), (1 << 27, False)]:
+            cfg = _cfg(Hq=Hq, Hkv=Hq // 8, dtype=dtype)
+            assert (L.yoco_cross_decode_tree_workspace_size(1, 1, 64, cfg) > 0) == ok
+            if not ok:
+                assert L.yoco_cross_decode_tree(FAKE, FAKE, FAKE, FAKE, FAKE, 100, FAKE, FAKE, None, None, 1, 1, 64, FAKE,
+                                                None, FAKE, 1 << 60, cfg, None) == yoco.ERR_UNSUPPORTED
+                assert L.yoco_swa_decode_tree(FAKE, FAKE, FAKE, FAKE, None, None, 1, 1, 64, FAKE, FAKE, FAKE, FAKE, None,
+                                              FAKE, 1 << 60, cfg, None) == yoco.ERR_UNSUPPORTED
+
+
 def test_workspace_sizes():
     sizes = [yoco.cross_decode_tree_workspace_size(B, N, M, 32, 8, 128, torch.bfloat16)
              for B, N, M in [(32, 1, 64), (1, 1, 131072), (4, 16, 65536), (16, 64, 131072)]]
