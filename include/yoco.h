@@ -319,11 +319,12 @@ yoco_status yoco_gret_decode(const void *q, const void *k, const void *v, const 
  *
  * yoco_rope: q [B, T, Hq, D], k [B, T, Hkv, D] (either may be NULL, with its
  * output; a decode step has T = 1); q_out, k_out like q, k: the same buffer (in
- * place) or one that does not overlap it.  pos: device int64 [B, T], or NULL:
+ * place) or one that overlaps neither the inputs nor the other output
+ * (YOCO_ERR_INVALID otherwise).  pos: device int64 [B, T], or NULL:
  * token t of every sequence is at pos0 + t.  backward nonzero: q and k are the
  * gradients of the rotated Q and K, and the outputs the gradients before the
  * rotation (the turn by -t, with the same mscale).
- * YOCO_ERR_UNSUPPORTED: rot_dim > D. */
+ * YOCO_ERR_UNSUPPORTED: rot_dim > D, more than 2^24 heads. */
 enum { YOCO_ROPE_HALF = 0, YOCO_ROPE_INTERLEAVED = 1 };
 enum { YOCO_ROPE_NONE = 0, YOCO_ROPE_LINEAR = 1, YOCO_ROPE_NTK = 2, YOCO_ROPE_BY_PARTS = 3 };
 typedef struct {

@@ -449,9 +449,19 @@ yoco_status yoco_rope(const void *q, const void *k, int32_t B, int64_t T, const 
     if (B == 0 || T == 0) return YOCO_OK;
     if ((!q && !k) || !ok_opt(q) || !ok_opt(k) || !ok_opt(q_out) || !ok_opt(k_out) || !ok_opt(pos))
         return YOCO_ERR_INVALID;
+    if ((int64_t)cfg->Hq + cfg->Hkv > 1 << 24) return YOCO_ERR_UNSUPPORTED;   // a CTA counts its units in 32 bits
+    const int64_t n = B * T, head = (int64_t)cfg->D * dtype_bytes(cfg->dtype);
+    if (n > INT64_MAX / 2 / (cfg->Hq * head)) return YOCO_ERR_UNSUPPORTED;
+    // in place, or apart from everything that is read
+    const int64_t q_bytes = n * cfg->Hq * head, k_bytes = n * cfg->Hkv * head;
+    if ((q_out != q && overlap(q_out, q_bytes, q, q_bytes)) || (k_out != k && overlap(k_out, k_bytes, k, k_bytes)) ||
+        overlap(q_out, q_bytes, k, k_bytes) || overlap(k_out, k_bytes, q, q_bytes) ||
+        overlap(q_out, q_bytes, k_out, k_bytes) || overlap(q_out, q_bytes, pos, 8 * n) ||
+        overlap(k_out, k_bytes, pos, 8 * n))
+        return YOCO_ERR_INVALID;
     RopeArgs a;
     a.q = q; a.k = k; a.q_out = q_out; a.k_out = k_out; a.pos = pos;
-    a.n = B * T; a.T = T; a.pos0 = pos0;
+    a.n = n; a.T = T; a.pos0 = pos0;
     a.Hq = cfg->Hq; a.Hkv = cfg->Hkv; a.D = cfg->D; a.dtype = cfg->dtype;
     a.rot_dim = rope->rot_dim; a.interleaved = rope->layout == YOCO_ROPE_INTERLEAVED; a.backward = backward != 0;
     a.mscale = (float)rope->mscale; a.inv_freq = rope->inv_freq;

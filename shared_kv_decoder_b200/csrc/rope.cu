@@ -147,7 +147,6 @@ cudaError_t launch_l(const RopeArgs &a, const RopeParams &p, dim3 grid, cudaStre
 }  // namespace
 
 cudaError_t launch_rope(const RopeArgs &a, cudaStream_t st) {
-    if ((int64_t)a.Hq + a.Hkv > 1 << 24) return cudaErrorNotSupported;   // a CTA counts its units in 32 bits
     RopeParams p;
     p.q = a.q; p.k = a.k; p.q_out = a.q_out; p.k_out = a.k_out; p.pos = a.pos;
     p.n = a.n; p.T = a.T; p.pos0 = a.pos0;

@@ -137,3 +137,25 @@ def test_graph_and_refusals(cuda_lib):
         cuda_lib.rope(q.transpose(1, 2), None, cfg)
     with pytest.raises(cuda_lib.YocoError):      # more than the head has
         cuda_lib.rope(q, k, cuda_lib.rope_config(128), pos=pos)
+
+
+def test_outputs_side_by_side_and_shifted(cuda_lib):
+    """Outputs that touch the inputs' buffers are taken, ones that overlap them refused."""
+    T, H, D = 4, 2, 64
+    buf = wl.normal((5, T, H, D), 2050).cuda()
+    keep = buf.clone()
+    cfg = cuda_lib.rope_config(64)
+    q, k = buf[None, 1], buf[None, 3]
+    want = cuda_lib.rope(q, k, cfg, pos0=9)
+    cuda_lib.rope(q, k, cfg, pos0=9, q_out=buf[None, 2], k_out=buf[None, 4])
+    assert torch.equal(buf[None, 2], want[0]) and torch.equal(buf[None, 4], want[1])
+    assert torch.equal(buf[[0, 1, 3]], keep[[0, 1, 3]])
+    flat = buf.view(1, 5 * T, H, D)
+    for bad in [dict(q_out=flat[:, T + 1:2 * T + 1]), dict(q_out=k), dict(k_out=q), dict(k_out=flat[:, 3 * T - 1:4 * T - 1]),
+                dict(q_out=buf[None, 0], k_out=buf[None, 0])]:
+        before = buf.clone()
+        with pytest.raises(cuda_lib.YocoError):
+            cuda_lib.rope(q, k, cfg, pos0=9, **bad)
+        assert torch.equal(buf, before)
+    cuda_lib.rope(q, k, cfg, pos0=9, q_out=q, k_out=k)
+    assert torch.equal(buf[None, 1], want[0]) and torch.equal(buf[None, 3], want[1])

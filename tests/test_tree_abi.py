@@ -81,6 +81,31 @@ def test_rope_arguments_rejected_before_launch():
     assert call(B=0) == yoco.OK and call(T=0) == yoco.OK
 
 
+def test_rope_outputs_in_place_or_apart():
+    L = yoco.load()
+    B, T, Hq, Hkv, D = 2, 5, 8, 2, 64
+    at = lambda base, byte: ctypes.c_void_p(base.value + byte)
+    q, k, pos, a, b = [ctypes.c_void_p(0x1000000 * i) for i in range(1, 6)]
+    rope = yoco.rope_config(64)
+    for dtype, size in ((0, 2), (1, 4)):
+        qb, kb, pb = B * T * Hq * D * size, B * T * Hkv * D * size, 8 * B * T
+
+        def call(qo, ko, p=pos):
+            return L.yoco_rope(q, k, B, T, p, 0, 0, qo, ko, ctypes.byref(rope), _cfg(Hq, Hkv, D, dtype), None)
+        for what, size_ in [(k, kb), (pos, pb), (b, kb)]:
+            for byte in (0, size_ - 16, 16 - qb):
+                assert call(at(what, byte), b) == yoco.ERR_INVALID
+        for what, size_ in [(q, qb), (pos, pb), (a, qb)]:
+            for byte in (0, size_ - 16, 16 - kb):
+                assert call(a, at(what, byte)) == yoco.ERR_INVALID
+        for byte in (16, qb - 16, -16, 16 - qb):
+            assert call(at(q, byte), b) == yoco.ERR_INVALID
+        for byte in (16, kb - 16, -16, 16 - kb):
+            assert call(a, at(k, byte)) == yoco.ERR_INVALID
+    # more bytes than an address has
+    assert L.yoco_rope(q, k, 1 << 30, 1 << 30, None, 0, 0, a, b, ctypes.byref(rope), _cfg(), None) == yoco.ERR_UNSUPPORTED
+
+
 def test_cross_decode_tree_arguments_rejected_before_launch():
     L = yoco.load()
     B, N, M, R = 4, 16, 65536, 1 << 20
