@@ -29,8 +29,9 @@ constexpr int kSimtKeys = 64;   // BN of the CUDA-core kernels
 constexpr int kMergeWarps = 8;
 constexpr int kGroupHeads = 8;
 // tiles of a CTA of a cluster at most, by whether the clusters fill half the GPU
-// (16 nodes over 2 x 8000 tokens, 16 tiles in clusters on 64 SMs, 26.1 us, as
-// shares 23.7; over 4 x 7900, on 128 SMs, 27.3 and 33.6)
+// (16 nodes, 16 tiles a CTA: 2 x 8059 tokens in clusters on 64 SMs 23.4 us, as
+// shares 21.9; 4 x 8059, on 128 SMs, 29.6 and 35.0; 12 tiles a CTA: 2 x 6011
+// tokens 19.6 and 19.8)
 constexpr int kClusterTiles = 16, kFewClusterTiles = 12;
 
 // A tile of the fp32 kernels: where its keys are, and how many there are.
@@ -127,9 +128,11 @@ YOCO_DEV void store_four(const Params &p, const Seg &g, int r, int col4, float m
 
 }  // namespace
 
-// fp32 on the CUDA cores, up to 32 rows of a KV head: bound by issue slots
-// (69% taken; two tiles are on their way while one computes).  A warp has eight rows and KW keys of every tile, with statistics of
-// its own, so that nothing is exchanged before the segment ends.  A lane has CPL
+// fp32 on the CUDA cores, up to 32 rows of a KV head: instructions bound it more
+// than anything else does (69% of the issue slots are taken, 40-45% of the FMA
+// pipe, 34-55% of DRAM; two tiles are on their way while one computes).  A warp
+// has eight rows and KW keys of every tile, with statistics of its own, so that
+// nothing is exchanged before the segment ends.  A lane has CPL
 // columns of q, K, V and o: K and V are read from shared memory once, in whole
 // rows, and q stays in registers.  The columns' sums for four keys by eight rows
 // are exchanged so that a lane ends with one of the 32 scores; its q and K are
@@ -308,8 +311,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) tree_few_kernel(const __grid_c
     }
 }
 
-// fp32 on the CUDA cores, more rows: bound by reading operands from shared memory,
-// then by the FMA pipe.  256 threads for 16 RT rows x 64 keys; thread (ty, tx) of a
+// fp32 on the CUDA cores, more rows: operands are read from shared memory for
+// every few FMAs, and no unit is full (69% of the issue slots, 57% of the FMA
+// pipe).  256 threads for 16 RT rows x 64 keys; thread (ty, tx) of a
 // 16 x 16 grid holds the rows ty + 16 i: in S = q K^T the keys tx + 16 j, in O += P V
 // the columns 4 tx + 64 j.  V is copied while S is computed, the next K during P V.
 // A row's statistics are the same in its 16 threads; unseen keys as in the kernel
@@ -637,11 +641,16 @@ bool make_tree_plan(int32_t B, int32_t N, int64_t max_len, int Hq, int Hkv, int 
     const int n_rt = (N * (Hq / Hkv) + pl.rows - 1) / pl.rows;
     const int64_t stream_tiles = (max_len + pl.keys - 1) / pl.keys + 1;
     // bf16, few streams, none of them long: a cluster a stream, no second launch
-    // and no numbering to work out first (16 nodes over 1 x 2047 tokens 12.3 us,
-    // as shares 19.3; over 8 x 3900 28.0 and 38.5; over 1 x 15000 25.4 and 26.5).
+    // and no numbering to work out first (16 nodes over 1 x 1915 tokens 10.4 us,
+    // as shares 16.8; over 4 x 3963 17.2 and 20.9; over 8 x 3963 30.0 and 34.7).
     // All clusters have to run at once -- 16 clusters of eight took two rounds
-    // and lost to the shares -- and the GPU's partitions hold 15 of eight CTAs this
-    // big, 33 of four and 74 of two.
+    // and lost to the shares -- and the 148 SMs' partitions hold 15 of eight CTAs
+    // this big, 33 of four and 74 of two.  The limits on tiles are safe ones for one
+    // row tile.  What they give away: two row tiles lose from about six tiles a CTA
+    // on unless the clusters fill half the GPU (64 nodes over 2 x 6011 tokens 35.7 us
+    // in clusters, 27.4 as shares), and one row tile would gain past the limits (16
+    // nodes over 1 x 15227 tokens 23.1 and 24.5, over 4 x 12155 39.6 and 44.7; two
+    // streams of 15227 tokens 22.1 and 31.1).
     const int sms = device_sm_count(), room[3] = {sms / 2, (sms - 16) / 4, (sms - 28) / 8};
     pl.cluster = 0;
     if (dtype == kBF16)

@@ -6,9 +6,11 @@
 // sequence's keys in tiles of BN -- first the context (the cache's rows, or the
 // ring's slots), then one tile with the drafted nodes' own keys.  The CTAs come
 // in groups of `heads`, one KV head each, which walk the same tiles side by
-// side: a token's K (or V) of all heads is one run in memory (8 heads of 128:
-// 64 nodes over 131007 tokens 189 us, 197 us in groups of one; 16 sequences of
-// 64K-128K tokens 1034 and 1028 us).
+// side: a token's K (or V) of all heads is one run in memory.  It matters where
+// the keys come from DRAM and segments are short (8 heads of 128, 64 sequences x
+// 48 nodes over the 1024 ring, caches flushed: 121 us, 127 in groups of one; with
+// the ring in L2 119 and 118), and no more over long contexts (64 nodes over
+// 131007 tokens 160 and 158, 16 sequences of 64K-128K tokens 976-1047 and 990-996).
 // The tiles of (sequence, row block, head block) are numbered sequence by
 // sequence, and group c of C takes a contiguous share of the T tiles, T / C of
 // them to within one: every CTA gets the same work whatever the lengths are,
@@ -16,9 +18,9 @@
 // more tiles a group (kAlignSlack) let every stream be cut into parts of `part`
 // tiles with no group holding pieces of two, it is cut so: a second segment
 // costs a CTA another fill and drain of its pipeline, as long as about five
-// tiles (4 sequences x 16 nodes over the 1024 ring, before clusters took that
-// case: CTAs of one segment ran 11 us, those of two 17).  The streams are then
-// numbered as if they were a multiple of `part` long.  A CTA's part of a stream
+// tiles (16 nodes over the 1024 ring, 12 sequences: 21 us, cut anywhere 27; 16
+// sequences: 22 and 35; on the other side 12 x 8000 tokens, 81 and 78).  The
+// streams are then numbered as if they were a multiple of `part` long.  A CTA's part of a stream
 // is a segment.  A stream that one CTA has whole is finished by it; of one that
 // is shared, each CTA leaves a partial (m, l, unnormalised o) in the workspace,
 // slot 0 for the segment its share opens with, slot 1 for the one it ends with,

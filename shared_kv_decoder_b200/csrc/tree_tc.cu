@@ -16,18 +16,13 @@
 // read is the longer one up to about R = 250.  Measured (graph replays on
 // several GPUs): 16 x 64K-128K tokens, 16 nodes (R = 64): 930-1075 us,
 // 5.9-6.8 TB/s of the cache, the clock at 1.3-1.5 GHz under the power cap;
-// 131007 tokens, 64 nodes (R = 256): 163-167 us, 825-843 TFLOP/s, the chain of
+// 131007 tokens, 64 nodes (R = 256): 159-179 us, 768-865 TFLOP/s, the chain of
 // one tile's softmax (1850 cycles) and the MMAs that wait for it (about 2000) the
-// limit, tensor pipe half busy; 64 x 48 nodes over the 1024 ring: 113-117 us, a
+// limit, tensor pipe half busy; 64 x 48 nodes over the 1024 ring: 117-120 us, a
 // segment's start and end (nine tiles) a quarter of it; in clusters 2047 tokens
-// 10.5 us, 4 x 16 nodes over the ring 12.8, latency throughout.
-// Two warps a row, 64 columns each, so that the softmax takes 1200 cycles, were
-// slower all the same (1050 for 1007 us, 155 for 142): the two have to agree on
-// the reference, and the power cap takes the rest.  All exponentials are MUFU's:
-// one pair in eight by a polynomial on the FMA pipe paid while the softmax warps
-// had 168 registers (137 for 162 us on the ring), with 216 it costs 2-3% (120 for
-// 117).  The first 64 weights formed by the old reference, with the maximum in
-// their shadow, were no faster (166 for 166) and slower on the ring (142 for 117).
+// 10.5 us, 4 x 16 nodes over the ring 12.8, latency throughout.  One warp has a
+// whole row, so that nothing is agreed on between warps, and all exponentials
+// are MUFU's.
 //
 // Warp roles (384 threads):
 //   warps 0-3, 4-7  softmax chains A and B: thread r owns row r (TMEM lane r)
@@ -39,8 +34,7 @@
 //   warps 9, 11     MMA issue of chain A and of chain B, one thread each: a wait or
 //                   a commit takes about a hundred cycles of its thread even when
 //                   nothing is left to wait for, and with one thread for both
-//                   chains these, not the tensor core, set the pace (16 x 64K-128K
-//                   tokens on one GPU: 1180 us, 1074 with two threads in turns)
+//                   chains these, not the tensor core, set the pace
 // TMEM (512 columns): S_A/P_A, S_B/P_B, O_A, O_B, 128 columns each; P is bf16
 // over the first 64 columns of its S.
 //
@@ -290,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     // registers: 384 x 168 at the launch, 128 x 72 + 256 x 216 from here (with 168 for
-    // all, 131 us for the 120 of 64 x 48 nodes over the 1024 ring, 184 for the 177 of
+    // all, 159 us for the 120 of 64 x 48 nodes over the 1024 ring, 180 for the 160 of
     // 64 nodes over 131007 tokens)
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
