@@ -351,7 +351,8 @@ yoco_status yoco_rope(const void *q, const void *k, int32_t B, int64_t T, const 
  *
  * Shared by both trees
  *  - q, o [B, N, Hq, D]; k_nodes, v_nodes [B, N, Hkv, D]; 1 <= N <= 64
- *    (YOCO_ERR_UNSUPPORTED above).
+ *    (YOCO_ERR_UNSUPPORTED above, with more than 2^24 heads, and where the
+ *    tiles at full length or B N Hq pass 2^30).
  *  - tree_mask: device uint64 [B, N]: bit j of tree_mask[b][i] set lets node i
  *    see node j (its ancestors, and itself: nothing is implied).  NULL: a
  *    chain, node i sees nodes 0..i.
